@@ -1,0 +1,171 @@
+/*
+ * spec_verify_cache.h -- C ABI of the operators on the KV cache around the
+ * verify step: the verifier's attention of the new tokens over the cache, the
+ * commit of the accepted path into it (in bf16 or quantised to 8 bits), and
+ * the way back from the quantised cache.
+ *
+ * "Speculative decoding -- draft, verify, repeat" (factory.pai-world.com,
+ * lesson 07-16): the verifier scores all drafts in one forward pass (section
+ * "Core algorithm", step 2), candidate trees are scored with tree attention
+ * (section on Medusa), and the pass's KV entries are committed or dropped
+ * after the verify (section "KV cache dance").  The pages give no code for
+ * any of them, and say nothing on 8-bit caches.
+ *
+ * Caches keep spec_verify_kv_commit's layout: a plane is the K or the V half
+ * of one layer, [B][max_len][heads][head_dim], and a sequence's first
+ * cache_len[b] rows are its prefix.  Two formats:
+ *   SV_KV_BF16  bf16 values
+ *   SV_KV_E4M3  e4m3 codes (1 sign, 4 exponent, 3 mantissa bits; largest
+ *               448), and beside them one scale byte s for every (row, head),
+ *               [B][max_len][heads]: a code c stands for c * 2^(s - 127).
+ * Everything is caller-owned device memory, asynchronous on `stream`
+ * (cudaStream_t, NULL = legacy default stream) on the current device; nothing
+ * is allocated and nothing synchronises, so every call can be captured into a
+ * CUDA graph.  Host errors enqueue nothing.
+ */
+#ifndef SPEC_VERIFY_CACHE_H
+#define SPEC_VERIFY_CACHE_H
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include "spec_verify.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+typedef enum { SV_KV_BF16 = 0, SV_KV_E4M3 = 1 } sv_kv_format;
+
+/*
+ * Commit of the accepted path: appends rows of the verifier's scratch to the
+ * cache, as spec_verify_kv_commit does for a chain, for chains and for the
+ * paths of spec_verify_tree_run, and quantises them on the way when the cache
+ * is SV_KV_E4M3.
+ *   rows         bf16 [planes][B][T][heads][head_dim], the entries of the T
+ *                tokens of the verifier's pass; may be NULL when T == 0
+ *   cache        [planes][B][max_len][heads][head_dim] in `format`
+ *   scale        uint8 [planes][B][max_len][heads] (SV_KV_E4M3 only, else NULL)
+ *   cache_len    int32 [B]: rows already in the cache
+ *   out_len      int32 [B]: receives the new lengths; may be cache_len itself
+ *   num_accepted int32 [B], as written by the verify (-1 = invalid sequence)
+ *   path         int32 [B][T] or NULL: entry i is the row of `rows` that holds
+ *                the i-th accepted draft (spec_verify_tree_run's path_nodes,
+ *                with T = M + 1); NULL: row lead + i (a chain)
+ *   lead         rows 0 .. lead - 1 are committed ahead of the accepted ones
+ *                (1: the pass's first token, whose entry is not in the cache
+ *                yet; 0: drafts only)
+ * Per sequence: lead + num_accepted rows go to cache rows cache_len[b] ...
+ * num_accepted < 0 commits nothing (not the lead rows either) and keeps the
+ * length; lead + num_accepted > T commits nothing and sets SV_KV_BAD_COUNT; a
+ * length outside [0, max_len - rows] commits nothing and sets SV_KV_OVERFLOW;
+ * a path entry outside [0, T) among the accepted commits nothing and sets
+ * SV_KV_BAD_PATH.  The bits are OR-ed into *status (device int32, may be
+ * NULL; the caller clears it).  Cache rows that receive nothing, and their
+ * scales, are left as they were.
+ *
+ * Quantisation of one (row, head): e is the smallest whole number in
+ * [-40, 120] with max|x| <= 448 * 2^e (over the finite elements); codes are
+ * x * 2^-e rounded to nearest, ties to even; the scale byte is e + 127.  A NaN or
+ * an infinity becomes the NaN code and sets SV_KV_NONFINITE.  A power of two
+ * keeps the scaling exact, so the codes' rounding (half a step: 2^-4 of the
+ * value, 2^-10 * 2^e below 2^-6 * 2^e) is the only one.
+ *
+ * SV_ERR_INVALID_ARG: negative sizes, planes < 1, heads < 1, lead < 0 or > T,
+ * head_dim not a multiple of 16 in 16 .. 256, a needed pointer NULL, rows or
+ * cache not 16-byte aligned; SV_ERR_DTYPE: unknown format; SV_ERR_TOO_LARGE:
+ * more than 65535 sequences, T > 1024 or byte offsets that would pass 2^62.
+ * One kernel launch.
+ */
+enum { SV_KV_BAD_PATH = 4, SV_KV_NONFINITE = 8 };
+
+sv_status spec_verify_kv_commit_path(const void *rows, void *cache, uint8_t *scale, const int32_t *cache_len,
+                                     int32_t *out_len, const int32_t *num_accepted, const int32_t *path,
+                                     int32_t *status, int planes, int B, int T, int lead, int max_len, int heads,
+                                     int head_dim, sv_kv_format format, void *stream);
+
+/*
+ * Reads an SV_KV_E4M3 cache back as bf16: rows start[b] .. cache_len[b] - 1
+ * of every sequence, at most n of them, to out rows 0 ..
+ *   cache, scale as above; cache_len int32 [B]; start int32 [B] or NULL (0)
+ *   out  bf16 [planes][B][n][heads][head_dim]; rows past a sequence's last
+ *        one are left as they were
+ * A code times its scale is exact in bf16 (4 significant bits), but for scales
+ * so small that the product is below bf16's smallest normal 2^-126 (never
+ * written by the commit).  A NaN code gives NaN.  A length outside
+ * [0, max_len] or a negative start reads nothing of that sequence and sets
+ * SV_KV_OVERFLOW in *status (may be NULL).
+ * Host errors as for the commit (n in T's place, without its limit).  One kernel launch.
+ */
+sv_status spec_verify_kv_read(const void *cache, const uint8_t *scale, const int32_t *cache_len,
+                              const int32_t *start, void *out, int32_t *status, int planes, int B, int n,
+                              int max_len, int heads, int head_dim, void *stream);
+
+/*
+ * The verifier's attention of T new tokens a sequence.  Query head i of token
+ * t of sequence b, with key/value head i / (heads_q / heads_kv), sees
+ *   - the shared prefix (every sequence and token; its rows are one copy that
+ *     all sequences' queries share, read once for all of them),
+ *   - the sequence's own cache, rows 0 .. cache_len[b] - 1,
+ *   - of the new tokens, itself and its ancestors,
+ * and out = sum_j exp(x_j) v_j / sum_j exp(x_j), x_j = softmax_scale * (q . k_j).
+ * With no key at all, out is 0 and lse is -inf.
+ *
+ * All fields are 8 bytes wide.  Pointers are device memory; those of bf16 and
+ * e4m3 data 16-byte aligned.
+ */
+typedef struct {
+    const void *q;              /* bf16 [B][T][heads_q][head_dim], strides below */
+    const void *k_cache;        /* [B][max_len][heads_kv][head_dim] in `format`; may be NULL when max_len == 0 */
+    const void *v_cache;
+    const uint8_t *k_scale;     /* [B][max_len][heads_kv], SV_KV_E4M3 only */
+    const uint8_t *v_scale;
+    const int32_t *cache_len;   /* [B]; may be NULL when max_len == 0 */
+    const void *k_prefix;       /* [prefix_len][heads_kv][head_dim] in `format`; NULL when prefix_len == 0 */
+    const void *v_prefix;
+    const uint8_t *k_prefix_scale; /* [prefix_len][heads_kv], SV_KV_E4M3 only */
+    const uint8_t *v_prefix_scale;
+    const void *k_new;          /* bf16 [B][T][heads_kv][head_dim], strides below; NULL: the queries see no */
+    const void *v_new;          /* new token (theirs are in the cache already) */
+    const int32_t *parent;      /* [B][T]: parent[b][0] = -1, 0 <= parent[b][t] < t (as spec_verify_tree_run's); */
+                                /* NULL: a chain, parent[b][t] = t - 1; not read when k_new is NULL */
+    void *out;                  /* bf16 [B][T][heads_q][head_dim], contiguous */
+    float *lse;                 /* [B][T][heads_q]: ln sum_j exp(x_j); may be NULL */
+    int32_t *status;            /* SV_ATTN_* bits are OR-ed into it; may be NULL */
+    void *workspace;            /* spec_verify_attention_workspace bytes, 16-byte aligned; calls that can */
+    int64_t workspace_bytes;    /* overlap on the GPU need one each; its content does not matter */
+    int64_t q_stride_b, q_stride_t;     /* elements between sequences and tokens; the last two dimensions are */
+    int64_t new_stride_b, new_stride_t; /* contiguous.  Multiples of 8 (views into a fused projection). */
+    int64_t B, T, heads_q, heads_kv, head_dim, max_len, prefix_len;
+    int64_t format;             /* sv_kv_format of cache and prefix */
+    double softmax_scale;       /* positive and finite */
+} sv_attention_args;
+
+/*
+ * A sequence whose cache_len is outside [0, max_len] sets SV_ATTN_BAD_LEN, one
+ * whose parent entries break their rule SV_ATTN_BAD_TREE; its out and lse are
+ * NaN, and nothing out of range is read.  Keys and values that a token
+ * does not see do not matter, NaN and infinities among them; a NaN or infinity
+ * in v_new makes the tokens that see it NaN in all columns.  SV_ATTN_TIMEOUT:
+ * a bounded wait inside the kernel gave up; the outputs are then invalid.
+ *
+ * SV_ERR_INVALID_ARG: a NULL args, sizes below 1 (max_len and prefix_len below
+ * 0), heads_q not a multiple of heads_kv, T > 128, a stride or alignment as above violated,
+ * a needed pointer NULL, a scale that is not positive and finite, a workspace
+ * too small; SV_ERR_SHAPE: head_dim other than 64 and 128; SV_ERR_DTYPE:
+ * unknown format; SV_ERR_TOO_LARGE: B * T * heads_q or a count of tiles past
+ * 2^31 - 1; SV_ERR_CUDA: a driver or runtime call failed.  B == 0 enqueues nothing.
+ * Two kernel launches.
+ */
+enum { SV_ATTN_BAD_LEN = 1, SV_ATTN_BAD_TREE = 2, SV_ATTN_TIMEOUT = 4 };
+
+/* Bytes of workspace for a call with these sizes and pointers (host arithmetic only). */
+sv_status spec_verify_attention_workspace(const sv_attention_args *args, int64_t *bytes);
+
+sv_status spec_verify_attention(const sv_attention_args *args, void *stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* SPEC_VERIFY_CACHE_H */

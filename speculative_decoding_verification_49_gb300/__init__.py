@@ -1,7 +1,8 @@
 """GB300 speculative-sampling verify step.
 
 Python binding of ``libspecverify.so`` (the CUDA kernels behind the C ABI in
-``include/spec_verify.h``).  The functions named ``spec_verify_*`` mirror the
+``include/spec_verify.h``, and for the KV cache ``include/spec_verify_cache.h``).
+The functions named ``spec_verify_*`` mirror the
 C entry points one to one and take raw device pointers; ``SpecVerify`` is a
 convenience wrapper that takes torch tensors and only marshals arguments.
 Every step of the verify computation runs in the CUDA library: there is no
@@ -12,6 +13,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 
 from .build import LIBRARY
 
@@ -59,6 +61,24 @@ _SIGNATURES = [
 SV_KV_OVERFLOW = 1
 SV_KV_BAD_COUNT = 2
 
+# the entry points of include/spec_verify_cache.h
+_CACHE_SIGNATURES = [
+    ("spec_verify_kv_commit_path", _I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P]),
+    ("spec_verify_kv_read", _I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
+    ("spec_verify_attention_workspace", _I, [ctypes.c_char_p, ctypes.POINTER(ctypes.c_int64)]),
+    ("spec_verify_attention", _I, [ctypes.c_char_p, _P]),
+]
+
+SV_KV_BAD_PATH = 4
+SV_KV_NONFINITE = 8
+
+SV_KV_BF16 = 0
+SV_KV_E4M3 = 1
+
+SV_ATTN_BAD_LEN = 1
+SV_ATTN_BAD_TREE = 2
+SV_ATTN_TIMEOUT = 4
+
 _lib = None
 
 
@@ -76,7 +96,7 @@ def load() -> ctypes.CDLL:
             raise ImportError(f"{LIBRARY} is missing: build it with "
                               "`python -m speculative_decoding_verification_49_gb300.build`")
         lib = ctypes.CDLL(LIBRARY)
-        for name, res, args in _SIGNATURES:
+        for name, res, args in _SIGNATURES + _CACHE_SIGNATURES:
             fn = getattr(lib, name)
             fn.restype = res
             fn.argtypes = args
@@ -85,7 +105,13 @@ def load() -> ctypes.CDLL:
 
 
 def exported_names():
+    """The entry points of include/spec_verify.h."""
     return [s[0] for s in _SIGNATURES]
+
+
+def exported_cache_names():
+    """The entry points of include/spec_verify_cache.h."""
+    return [s[0] for s in _CACHE_SIGNATURES]
 
 
 # ---- one-to-one wrappers of the C ABI (raw pointers as Python ints) ---------
@@ -181,6 +207,37 @@ def spec_verify_kv_commit(scratch, cache, cache_len, num_accepted, status, plane
     and advance cache_len (device pointers; asynchronous on stream)."""
     return load().spec_verify_kv_commit(scratch, cache, cache_len, num_accepted, status, planes, B, N,
                                         max_len, row_bytes, stream)
+
+
+def spec_verify_kv_commit_path(rows, cache, scale, cache_len, out_len, num_accepted, path, status, planes, B, T,
+                               lead, max_len, heads, head_dim, format, stream) -> int:
+    """Append each sequence's lead and accepted rows to its cache, in bf16 or
+    quantised to e4m3, and write the new lengths (device pointers; asynchronous)."""
+    return load().spec_verify_kv_commit_path(rows, cache, scale, cache_len, out_len, num_accepted, path, status,
+                                             planes, B, T, lead, max_len, heads, head_dim, format, stream)
+
+
+def spec_verify_kv_read(cache, scale, cache_len, start, out, status, planes, B, n, max_len, heads, head_dim,
+                        stream) -> int:
+    """Read rows of an e4m3 cache back as bf16 (device pointers; asynchronous)."""
+    return load().spec_verify_kv_read(cache, scale, cache_len, start, out, status, planes, B, n, max_len, heads,
+                                      head_dim, stream)
+
+
+# sv_attention_args: 15 pointers, the softmax status, workspace and size, 4 strides, 8 sizes, the scale
+_ATTENTION_ARGS = struct.Struct("=17Q1q4q8qd")
+
+
+def spec_verify_attention_workspace(args: bytes):
+    """(status, bytes) for packed sv_attention_args."""
+    n = ctypes.c_int64(0)
+    st = load().spec_verify_attention_workspace(args, ctypes.byref(n))
+    return st, n.value
+
+
+def spec_verify_attention(args: bytes, stream) -> int:
+    """The verifier's attention, from packed sv_attention_args (asynchronous)."""
+    return load().spec_verify_attention(args, stream)
 
 
 # ---- torch convenience wrapper -------------------------------------------------
@@ -396,6 +453,214 @@ def kv_commit(scratch, cache, cache_len, num_accepted, status=None, stream=None)
                                _ptr(status), P, B, N, max_len, row_bytes, s.cuda_stream)
     if st != SV_OK:
         raise SpecVerifyError(st, "spec_verify_kv_commit")
+
+
+def _kv_format(cache, scale, what):
+    """The sv_kv_format of a cache tensor, its scale tensor checked: uint8, one byte a (row, head)."""
+    import torch
+    if cache.dtype == torch.bfloat16:
+        if scale is not None:
+            raise ValueError(f"a bf16 {what} has no scales")
+        return SV_KV_BF16
+    if cache.dtype != torch.float8_e4m3fn:
+        raise ValueError(f"{what} must be bfloat16 or float8_e4m3fn, got {cache.dtype}")
+    if scale is None or scale.dtype != torch.uint8 or scale.shape != cache.shape[:-1] or not scale.is_contiguous() \
+            or scale.device != cache.device:
+        raise ValueError(f"an e4m3 {what} needs contiguous uint8 scales of shape {tuple(cache.shape[:-1])}")
+    return SV_KV_E4M3
+
+
+def _int32(name, t, shape, device):
+    import torch
+    if t.dtype != torch.int32 or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)} on {device}")
+
+
+def _on(device, call, *args):
+    """call(*args) with ``device`` current."""
+    import torch
+    if torch.cuda.current_device() == device.index:
+        return call(*args)
+    with torch.cuda.device(device):
+        return call(*args)
+
+
+def kv_commit_path(rows, cache, cache_len, num_accepted, path=None, lead=0, scale=None, out_len=None, status=None,
+                   stream=None):
+    """Torch front end of spec_verify_kv_commit_path: append the accepted path
+    of every sequence to its cache, quantised when the cache is e4m3.
+
+    rows [P, B, T, heads, head_dim] bf16 holds the entries of the pass's T
+    tokens, cache [P, B, max_len, heads, head_dim] is bf16, or float8_e4m3fn
+    with ``scale`` uint8 [P, B, max_len, heads]; cache_len and num_accepted are
+    int32 [B]; ``path`` is None (a chain) or int32 [B, T], tree_run's path_nodes;
+    ``lead`` rows are committed ahead of the accepted ones (1 for the pass's
+    root).  The new lengths go to ``out_len``, which is returned (None:
+    cache_len itself, advanced in place); ``status`` is an optional int32 [1]
+    that collects SV_KV_* bits.  Enqueues on the current torch stream (or
+    ``stream``) and does not synchronise."""
+    import torch
+    if rows.dim() != 5 or cache.dim() != 5 or rows.shape[:2] != cache.shape[:2] or rows.shape[3:] != cache.shape[3:]:
+        raise ValueError(f"rows {tuple(rows.shape)} and cache {tuple(cache.shape)} do not match")
+    if rows.dtype != torch.bfloat16 or not rows.is_contiguous() or not cache.is_contiguous() or not cache.is_cuda \
+            or rows.device != cache.device:
+        raise ValueError("rows must be bfloat16, rows and cache contiguous on one CUDA device")
+    fmt = _kv_format(cache, scale, "cache")
+    P, B, T, H, D = rows.shape
+    dev = cache.device
+    if out_len is None:
+        out_len = cache_len
+    _int32("cache_len", cache_len, (B,), dev)
+    _int32("out_len", out_len, (B,), dev)
+    _int32("num_accepted", num_accepted, (B,), dev)
+    if path is not None:
+        _int32("path", path, (B, T), dev)
+    if status is not None:
+        _int32("status", status, (1,), dev)
+    s = stream if stream is not None else torch.cuda.current_stream(dev)
+    st = _on(dev, spec_verify_kv_commit_path, _ptr(rows), _ptr(cache), _ptr(scale), _ptr(cache_len), _ptr(out_len),
+             _ptr(num_accepted), _ptr(path), _ptr(status), P, B, T, lead, cache.shape[2], H, D, fmt, s.cuda_stream)
+    if st != SV_OK:
+        raise SpecVerifyError(st, "spec_verify_kv_commit_path")
+    return out_len
+
+
+def kv_read(cache, scale, cache_len, start=None, rows=None, out=None, status=None, stream=None):
+    """Torch front end of spec_verify_kv_read: the rows start[b] (0 without
+    ``start``) .. cache_len[b] - 1 of an e4m3 cache [P, B, max_len, heads,
+    head_dim] as bf16, at most ``rows`` of them (max_len without it), in
+    ``out`` [P, B, rows, heads, head_dim] (zeros where a new one is made; rows
+    past a sequence's last one are left as they were).  Enqueues on the
+    current torch stream (or ``stream``) and does not synchronise."""
+    import torch
+    if cache.dim() != 5 or not cache.is_contiguous() or not cache.is_cuda or cache.dtype != torch.float8_e4m3fn:
+        raise ValueError("cache must be a contiguous float8_e4m3fn CUDA tensor [P, B, max_len, heads, head_dim]")
+    _kv_format(cache, scale, "cache")
+    P, B, L, H, D = cache.shape
+    dev = cache.device
+    s = stream if stream is not None else torch.cuda.current_stream(dev)
+    if out is None:
+        with torch.cuda.stream(s):
+            out = torch.zeros((P, B, L if rows is None else rows, H, D), dtype=torch.bfloat16, device=dev)
+    n = out.shape[2] if out.dim() == 5 else -1
+    if out.shape != (P, B, n, H, D) or (rows is not None and n != rows) or out.dtype != torch.bfloat16 \
+            or not out.is_contiguous() or out.device != dev:
+        raise ValueError("out must be contiguous bfloat16 [P, B, rows, heads, head_dim] on the cache's device")
+    _int32("cache_len", cache_len, (B,), dev)
+    if start is not None:
+        _int32("start", start, (B,), dev)
+    if status is not None:
+        _int32("status", status, (1,), dev)
+    st = _on(dev, spec_verify_kv_read, _ptr(cache), _ptr(scale), _ptr(cache_len), _ptr(start), _ptr(out), _ptr(status),
+             P, B, n, L, H, D, s.cuda_stream)
+    if st != SV_OK:
+        raise SpecVerifyError(st, "spec_verify_kv_read")
+    return out
+
+
+def _tokens(name, t, shape, device):
+    """Strides (between sequences, between tokens) of a bf16 [B, T, heads, head_dim] tensor whose last two
+    dimensions are contiguous."""
+    import torch
+    if t.dtype != torch.bfloat16 or t.shape != shape or t.device != device:
+        raise ValueError(f"{name} must be bfloat16 {tuple(shape)} on {device}, got {t.dtype} {tuple(t.shape)}")
+    sb, st, sh, sd = t.stride()
+    if (sd != 1 and shape[3] > 1) or (sh != shape[3] and shape[2] > 1):
+        raise ValueError(f"{name}'s heads and head_dim must be contiguous")
+    return sb if shape[0] > 1 else 0, st if shape[1] > 1 else 0
+
+
+def verify_attention(q, k_cache, v_cache, cache_len, k_new=None, v_new=None, parent=None, k_prefix=None,
+                     v_prefix=None, k_scale=None, v_scale=None, k_prefix_scale=None, v_prefix_scale=None, scale=None,
+                     out=None, lse=None, status=None, stream=None):
+    """Torch front end of spec_verify_attention: the attention of the T new
+    tokens of every sequence over [shared prefix | own cache | new tokens].
+
+    q [B, T, heads_q, D] bf16 (strides between sequences and tokens free, as in
+    a view of a fused projection), D 64 or 128; k_cache, v_cache [B, max_len,
+    heads_kv, D], bf16, or float8_e4m3fn with k_scale, v_scale uint8 [B,
+    max_len, heads_kv]; cache_len int32 [B].  k_new, v_new [B, T, heads_kv, D]
+    bf16 are the new tokens' own entries: token t sees itself and its ancestors
+    by ``parent`` (int32 [B, T], parent[b][0] = -1, as tree_run's; None: a
+    chain); without them the queries see the cache (and prefix) only.
+    k_prefix, v_prefix [prefix_len, heads_kv, D] of the cache's type, with
+    their scales, are one copy for the whole batch.  ``scale`` (default
+    1/sqrt(D)) multiplies the products.  ``lse`` float32 [B, T, heads_q]
+    receives the logarithms of the sums, ``status`` int32 [1] the SV_ATTN_*
+    bits.  Returns out [B, T, heads_q, D] bf16; enqueues on the current torch
+    stream (or ``stream``) and does not synchronise."""
+    import torch
+    if q.dim() != 4 or k_cache.dim() != 4 or not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor [B, T, heads_q, head_dim], the caches [B, max_len, heads_kv, head_dim]")
+    B, T, Hq, D = q.shape
+    L, H = k_cache.shape[1:3]
+    dev = q.device
+    qb, qt = _tokens("q", q, q.shape, dev)
+    if k_cache.shape != (B, L, H, D) or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype \
+            or k_cache.device != dev or v_cache.device != dev or not k_cache.is_contiguous() \
+            or not v_cache.is_contiguous():
+        raise ValueError(f"k_cache and v_cache must be contiguous [{B}, max_len, heads_kv, {D}] of one type")
+    fmt = _kv_format(k_cache, k_scale, "k_cache")
+    _kv_format(v_cache, v_scale, "v_cache")
+    _int32("cache_len", cache_len, (B,), dev)
+    nb = nt = 0
+    if (k_new is None) != (v_new is None) or (k_prefix is None) != (v_prefix is None):
+        raise ValueError("keys and values come together")
+    if k_new is not None:
+        nb, nt = _tokens("k_new", k_new, (B, T, H, D), dev)
+        if _tokens("v_new", v_new, (B, T, H, D), dev) != (nb, nt):
+            raise ValueError("k_new and v_new must have the same strides")
+        if parent is not None:
+            _int32("parent", parent, (B, T), dev)
+    elif parent is not None:
+        raise ValueError("parent goes with k_new and v_new")
+    Lp = 0
+    if k_prefix is not None:
+        Lp = k_prefix.shape[0]
+        for name, t, ts in (("k_prefix", k_prefix, k_prefix_scale), ("v_prefix", v_prefix, v_prefix_scale)):
+            if t.shape != (Lp, H, D) or t.dtype != k_cache.dtype or t.device != dev or not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous [prefix_len, {H}, {D}] of the cache's type")
+            _kv_format(t, ts, name)
+    if out is not None and (out.shape != q.shape or out.dtype != torch.bfloat16 or not out.is_contiguous()
+                            or out.device != dev):
+        raise ValueError("out must be contiguous bfloat16 of q's shape")
+    if lse is not None and (lse.shape != (B, T, Hq) or lse.dtype != torch.float32 or not lse.is_contiguous()
+                            or lse.device != dev):
+        raise ValueError("lse must be contiguous float32 [B, T, heads_q]")
+    if status is not None:
+        _int32("status", status, (1,), dev)
+    if scale is None:
+        scale = D ** -0.5
+    own = stream is None
+    s = torch.cuda.current_stream(dev) if own else stream
+
+    def p(t):
+        return 0 if t is None else t.data_ptr()
+
+    def packed(ws, nbytes):
+        return _ATTENTION_ARGS.pack(
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), p(k_scale), p(v_scale), cache_len.data_ptr(),
+            p(k_prefix), p(v_prefix), p(k_prefix_scale), p(v_prefix_scale), p(k_new), p(v_new), p(parent), p(out),
+            p(lse), p(status), ws, nbytes, qb, qt, nb, nt, B, T, Hq, H, D, L, Lp, fmt, scale)
+
+    st, nbytes = spec_verify_attention_workspace(packed(0, 0))
+    if st != SV_OK:
+        raise SpecVerifyError(st, "spec_verify_attention")
+    # the workspace comes from the caching allocator, for this call alone: calls on
+    # other streams and captured graphs each have their own
+    if own:
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        if out is None:
+            out = torch.empty((B, T, Hq, D), dtype=torch.bfloat16, device=dev)
+    else:
+        with torch.cuda.stream(s):
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            if out is None:
+                out = torch.empty((B, T, Hq, D), dtype=torch.bfloat16, device=dev)
+    st = _on(dev, spec_verify_attention, packed(ws.data_ptr(), nbytes), s.cuda_stream)
+    if st != SV_OK:
+        raise SpecVerifyError(st, "spec_verify_attention")
+    return out
 
 
 def lm_head_logits(hidden, weight, out=None, stream=None):

@@ -1,0 +1,135 @@
+"""The cache entry points on the CPU: exports, the C header, and every host-side refusal (nothing is launched)."""
+import ctypes
+import os
+import re
+import shutil
+import subprocess
+
+import pytest
+
+import speculative_decoding_verification_49_gb300 as sv
+from speculative_decoding_verification_49_gb300 import build as svbuild
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "spec_verify_cache.h")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    svbuild.build()
+    return sv.load()
+
+
+def declared():
+    text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+    return sorted(set(re.findall(r"\b(spec_verify_\w+)\s*\(", text)))
+
+
+def test_every_declared_symbol_is_exported(lib):
+    assert declared() == sorted(sv.exported_cache_names())
+    for name in declared():
+        assert hasattr(lib, name), name
+
+
+def test_header_is_plain_c_and_the_packed_struct_matches(tmp_path):
+    gcc = shutil.which("gcc")
+    if gcc is None:
+        pytest.skip("gcc not available")
+    src = os.path.join(ROOT, "tests", "c", "cache_usage.c")
+    exe = str(tmp_path / "cache_usage.o")
+    r = subprocess.run([gcc, "-std=c99", "-Wall", "-Wextra", "-Werror", "-pedantic", "-c", src, "-I",
+                        os.path.join(ROOT, "include"), "-o", exe], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    text = open(src).read()
+    for name in declared():
+        assert name + "(" in text, name
+    size = tmp_path / "size.c"
+    size.write_text('#include <stdio.h>\n#include "spec_verify_cache.h"\n'
+                    'int main(void) { printf("%d", (int)sizeof(sv_attention_args)); return 0; }\n')
+    exe = str(tmp_path / "size")
+    subprocess.run([gcc, str(size), "-I", os.path.join(ROOT, "include"), "-o", exe], check=True)
+    assert int(subprocess.run([exe], capture_output=True, text=True).stdout) == sv._ATTENTION_ARGS.size
+
+
+def _commit(rows=256, cache=512, scale=1024, cache_len=64, out_len=64, acc=128, path=None, status=None, planes=2, B=3,
+            T=4, lead=1, max_len=16, heads=2, D=64, fmt=sv.SV_KV_E4M3):
+    return sv.spec_verify_kv_commit_path(rows, cache, scale, cache_len, out_len, acc, path, status, planes, B, T, lead,
+                                         max_len, heads, D, fmt, None)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(planes=0), dict(B=-1), dict(T=-1), dict(lead=-1), dict(lead=5), dict(max_len=-1), dict(heads=0), dict(D=0),
+    dict(D=24), dict(D=272), dict(rows=None), dict(cache=None), dict(scale=None), dict(cache_len=None),
+    dict(out_len=None), dict(acc=None), dict(rows=264), dict(cache=520)])
+def test_commit_path_refusals(bad):
+    assert _commit(**bad) == sv.SV_ERR_INVALID_ARG
+
+
+def test_commit_path_other_codes():
+    assert _commit(fmt=2) == sv.SV_ERR_DTYPE
+    assert _commit(T=1025) == sv.SV_ERR_TOO_LARGE
+    assert _commit(B=65536) == sv.SV_ERR_TOO_LARGE
+    assert _commit(planes=1 << 30, max_len=1 << 30, heads=1024, D=256) == sv.SV_ERR_TOO_LARGE
+    assert _commit(B=0, rows=None, cache=None) == sv.SV_OK
+
+
+def _read(cache=512, scale=1024, cache_len=64, start=None, out=256, status=None, planes=2, B=3, n=4, max_len=16,
+          heads=2, D=64):
+    return sv.spec_verify_kv_read(cache, scale, cache_len, start, out, status, planes, B, n, max_len, heads, D, None)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(planes=0), dict(B=-1), dict(n=-1), dict(max_len=-1), dict(heads=0), dict(D=8), dict(D=40), dict(D=512),
+    dict(cache=None), dict(scale=None), dict(cache_len=None), dict(out=None), dict(cache=520), dict(out=264)])
+def test_read_refusals(bad):
+    assert _read(**bad) == sv.SV_ERR_INVALID_ARG
+
+
+def test_read_other_codes():
+    assert _read(B=65536) == sv.SV_ERR_TOO_LARGE
+    assert _read(planes=1 << 30, n=1 << 30, heads=1024, D=256) == sv.SV_ERR_TOO_LARGE
+    assert _read(B=0) == sv.SV_OK
+    assert _read(n=0) == sv.SV_OK
+
+
+GOOD = dict(q=256, k=512, v=1024, ks=0, vs=0, lens=64, kp=0, vp=0, kps=0, vps=0, kn=2048, vn=4096, parent=0, out=256,
+            lse=0, status=0, ws=512, nws=1 << 40, qb=4 * 6 * 64, qt=6 * 64, nb=4 * 2 * 64, nt=2 * 64, B=3, T=4, Hq=6,
+            H=2, D=64, L=100, Lp=0, fmt=0, scale=0.125)
+
+
+def _pack(**over):
+    return sv._ATTENTION_ARGS.pack(*{**GOOD, **over}.values())
+
+
+@pytest.mark.parametrize("code,bad", [
+    (sv.SV_ERR_INVALID_ARG, dict(B=-1)), (sv.SV_ERR_INVALID_ARG, dict(T=0)), (sv.SV_ERR_INVALID_ARG, dict(T=129)),
+    (sv.SV_ERR_INVALID_ARG, dict(Hq=0)), (sv.SV_ERR_INVALID_ARG, dict(H=0)), (sv.SV_ERR_INVALID_ARG, dict(Hq=7)),
+    (sv.SV_ERR_INVALID_ARG, dict(L=-1)), (sv.SV_ERR_INVALID_ARG, dict(Lp=-1)),
+    (sv.SV_ERR_SHAPE, dict(D=96)), (sv.SV_ERR_SHAPE, dict(D=256)), (sv.SV_ERR_DTYPE, dict(fmt=2)),
+    (sv.SV_ERR_INVALID_ARG, dict(scale=0.0)), (sv.SV_ERR_INVALID_ARG, dict(scale=-1.0)),
+    (sv.SV_ERR_INVALID_ARG, dict(scale=float("inf"))), (sv.SV_ERR_INVALID_ARG, dict(scale=float("nan"))),
+    (sv.SV_ERR_INVALID_ARG, dict(scale=1e39)), (sv.SV_ERR_INVALID_ARG, dict(scale=1e-60)),
+    (sv.SV_ERR_INVALID_ARG, dict(q=0)), (sv.SV_ERR_INVALID_ARG, dict(out=0)), (sv.SV_ERR_INVALID_ARG, dict(k=0)),
+    (sv.SV_ERR_INVALID_ARG, dict(v=0)), (sv.SV_ERR_INVALID_ARG, dict(lens=0)), (sv.SV_ERR_INVALID_ARG, dict(kn=0)),
+    (sv.SV_ERR_INVALID_ARG, dict(vn=0)), (sv.SV_ERR_INVALID_ARG, dict(Lp=5)),
+    (sv.SV_ERR_INVALID_ARG, dict(fmt=1)), (sv.SV_ERR_INVALID_ARG, dict(fmt=1, ks=16, vs=16, Lp=5, kp=16, vp=16)),
+    (sv.SV_ERR_INVALID_ARG, dict(q=264)), (sv.SV_ERR_INVALID_ARG, dict(k=520)), (sv.SV_ERR_INVALID_ARG, dict(vn=4104)),
+    (sv.SV_ERR_INVALID_ARG, dict(out=264)), (sv.SV_ERR_INVALID_ARG, dict(ws=520)),
+    (sv.SV_ERR_INVALID_ARG, dict(qb=4 * 6 * 64 + 4)), (sv.SV_ERR_INVALID_ARG, dict(qt=6 * 64 + 4)),
+    (sv.SV_ERR_INVALID_ARG, dict(nb=4 * 2 * 64 + 4)), (sv.SV_ERR_INVALID_ARG, dict(nt=2 * 64 + 4)),
+    (sv.SV_ERR_INVALID_ARG, dict(nt=0)), (sv.SV_ERR_INVALID_ARG, dict(nb=0)), (sv.SV_ERR_INVALID_ARG, dict(nws=0)),
+    (sv.SV_ERR_TOO_LARGE, dict(B=1 << 30)), (sv.SV_ERR_TOO_LARGE, dict(B=1 << 20, L=1 << 30)),
+])
+def test_attention_refusals(code, bad):
+    assert sv.spec_verify_attention(_pack(**bad), None) == code
+
+
+def test_attention_without_sequences_and_workspace():
+    assert sv.spec_verify_attention(_pack(B=0), None) == sv.SV_OK
+    assert sv.spec_verify_attention(None, None) == sv.SV_ERR_INVALID_ARG
+    st, n = sv.spec_verify_attention_workspace(_pack())
+    assert st == sv.SV_OK and n > 0
+    assert sv.spec_verify_attention(_pack(nws=n - 1), None) == sv.SV_ERR_INVALID_ARG
+    assert sv.spec_verify_attention_workspace(_pack(D=80))[0] == sv.SV_ERR_SHAPE
+    n_ptr = ctypes.POINTER(ctypes.c_int64)()
+    assert sv.load().spec_verify_attention_workspace(_pack(), n_ptr) == sv.SV_ERR_INVALID_ARG

@@ -1,142 +1,1195 @@
-// attention.cu -- the verifier's attention of new tokens over the KV cache.
-#include <climits>
-#include <cmath>
-#include <cstdint>
-
+// attention.cu -- the verifier's attention of T new tokens a sequence over
+// [shared prefix | own cache | new tokens], on the tcgen05 tensor cores of
+// sm_103a.
+//
+// "Speculative decoding -- draft, verify, repeat" (factory.pai-world.com,
+// lesson 07-16): the verifier scores all drafts in one pass (section "Core
+// algorithm", step 2), trees of candidates with tree attention (section on
+// Medusa).  The pages give the visibility rule (a token sees the context and
+// its own path) and no code.
+//
+// Mathematics.  For one key/value head h the rows of the product are the
+// (token, query head) pairs that share it: row R = (b*T + t)*G + g of B*T*G.
+// Each row keeps a reference mu, a sum l and an accumulator O over the keys
+// seen so far: with y_j = log2(e) * scale * q.k_j (plus the exponent of v_j's
+// scale for e4m3 values), w_j = 2^(y_j - mu + base), O = sum w_j v_j,
+// l = sum w_j (times 2^-exponent for e4m3).  mu follows the running maximum
+// lazily: O and l are rescaled only when the maximum has grown by more than a
+// few powers of two, which w's range absorbs.  Parts of a row that were computed
+// apart are joined as O = sum O_i 2^(R_i - R), R_i = mu_i - base.
+//
+// Work.  A segment is a block of up to 256 rows of one head with one key
+// source: all sequences' rows over the shared prefix (each prefix tile is read
+// once per 256 rows instead of once per sequence), or one sequence's rows
+// over its own cache and new tokens.  All segments' 128-key tiles form one
+// line that is cut into equal stretches, one per CTA (one CTA per SM), so
+// ragged lengths, few long sequences and many short ones all fill the machine;
+// a segment cut by a stretch's end leaves pieces that a second kernel joins, a
+// whole one (without a prefix) is written directly.
+//
+// A CTA has two accumulator slots.  A segment of more than 128 rows puts 128
+// rows in each and both use every key tile; with at most 128 rows both
+// hold the same rows and take alternate tiles, and are joined at the end.  Either way
+// one slot's softmax runs while the tensor cores work for the other.
+//   warps 0-3, 4-7  softmax and epilogue of slot 0, 1 (thread = row = TMEM lane)
+//   warp 8          TMA producer of a ring of 32 KiB stages (K and V tiles)
+//   warp 9          issues the MMAs: S = Q K^T (both from shared memory, 128 x
+//                   128 x D), O += P V (P from tensor memory, where it
+//                   overwrites S; V read in place, MN-major)
+//   warp 10         clears V rows that must not count (behind the length)
+//                   and non-finite values of new tokens, so that 0 * NaN cannot reach O
+// TMEM: O0, O1, S0, S1, 128 columns each.
+//
+// e4m3 caches stay in 8 bits in shared memory.  Q is split exactly into two
+// e4m3 terms (bf16 has 8 significant bits, a term 4; the tile's scale puts its
+// largest element into [224, 448], elements below 2^-18 of that lose bits), and
+// S is the sum of two kind::f8f6f4 products.  P goes into
+// three e5m2 terms: w rounded to f16 (11 bits), whose upper byte is an
+// e5m2 number; what is left is again f16.  base = 13 puts w's usual maximum at
+// 2^13 of e5m2's 2^15.8, and its smallest step 2^-16 is 2^-29 of that, so that
+// many light keys beside a heavy one keep their weight.  The new
+// tokens are bf16 and come first in their segment, with Q in bf16.
+//
+// Every wait is bounded (2 s); a kernel that gives up says so in *status.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+#include <climits>
+#include <cmath>
+#include <cstdint>
+#include <mutex>
+
 #include "spec_verify_cache.h"
-#include "sv_device.cuh"
+#include "sv_tc.cuh"
 
 namespace {
 
 using namespace sv;
 
 constexpr int kMaxT = 128;
+constexpr int kTile = 128;            // keys of a tile, rows of a slot
+constexpr int kSlotBytes = 32768;     // one ring stage
+constexpr int kVoff = 16384;          // V's place in a stage that holds K and V
+constexpr int kPanel = kTile * 128;   // 128 rows of 128 bytes
+constexpr int kSoftmaxThreads = 256;
+constexpr int kThreads = 352;
+constexpr int kMaxCtas = 160;         // of the grid; the workspace counts on it
+constexpr uint32_t kTmemCols = 512;
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr int kMaxStages = 6;
 
-struct Params {
-    sv_attention_args a;
+template <int D, bool E4> struct Cfg {
+    static constexpr int kQTile = kTile * D * 2;
+    static constexpr int kStages = D == 64 ? (E4 ? 5 : 6) : (E4 ? 4 : 5);
+    // keys and values of a bf16 tile fill a stage each when D = 128; all other tiles fit one stage together
+    static constexpr bool kTwo = D == 128;
+    static constexpr float kBase = E4 ? 13.0f : 0.0f;  // w's usual maximum is 2^base
+    static constexpr float kSlack = E4 ? 2.0f : 8.0f;  // growth of the maximum that w's range absorbs
 };
 
-__device__ __forceinline__ float code_scale(uint8_t s)
+struct AttnParams {
+    const __nv_bfloat16 *q;
+    const uint8_t *k_scale, *v_scale, *kp_scale, *vp_scale;
+    const int32_t *cache_len, *parent;
+    __nv_bfloat16 *out;
+    float *lse;
+    int32_t *status;
+    int32_t *seg_start;     // [B + 1] first unit of each sequence, written for the joining kernel
+    float *whole_p, *whole_s, *pieces;  // partial results: whole prefix segments, whole segments, cut segments
+    long long q_sb, q_st;
+    int B, T, Hq, H, G, L, Lp;
+    int has_new, max_len;
+    int nbp, ntp, UP;       // prefix: row blocks and tiles a head, units in all
+    int nbs;                // row blocks of a sequence's rows
+    int rp, rs, rm;         // rows of a slot in whole_p, whole_s, pieces
+    float c;                // softmax scale * log2(e)
+};
+
+struct Maps {
+    CUtensorMap k, v, kn, vn, kp, vp;
+};
+
+template <bool E4> struct Tables {};
+template <> struct Tables<true> {
+    float kk[2][2][kTile];   // per slot, alternating: the key's factor of S
+    float ev[2][2][kTile];   // exponent of the value's scale
+    float inv[2][2][kTile];  // 2^-exponent
+};
+
+template <bool E4> struct Ctl {
+    uint64_t full[kMaxStages];    // the stage's copies have landed
+    uint64_t empty[kMaxStages];   // the MMAs and the clearing warp are done with it
+    uint64_t fix[kMaxStages];     // the clearing warp has gone over it
+    uint64_t s_full[2];           // scores are in TMEM
+    uint64_t p_full[2];           // weights are in TMEM (one arrival per warp)
+    uint64_t o_full[2];           // the product with V is complete
+    uint64_t q_full;              // Q is in shared memory
+    uint64_t poison_full;         // poison holds this segment's new tokens
+    uint64_t done;
+    uint32_t poison_slot[kMaxStages][4];
+    uint32_t poison[4];           // new tokens with non-finite values
+    unsigned qmax[2];
+    int warp_sum[kThreads / 32];
+    int last_fill[kMaxStages];
+    uint32_t tmem;
+    int abort;
+    int start_b, start_ub;
+    Tables<E4> tab;
+};
+
+template <int D, bool E4> constexpr size_t smem_bytes()
 {
-    return s ? __int_as_float((int)s << 23) : __int_as_float(0x00400000);
+    return 1024 + 2 * (size_t)Cfg<D, E4>::kQTile + (size_t)Cfg<D, E4>::kStages * kSlotBytes + sizeof(Ctl<E4>);
+}
+static_assert(smem_bytes<128, false>() <= 232448 && smem_bytes<128, true>() <= 232448 &&
+                  smem_bytes<64, false>() <= 232448 && smem_bytes<64, true>() <= 232448,
+              "227 KiB of shared memory per CTA");
+
+__host__ __device__ __forceinline__ int cdiv(int a, int b)
+{
+    return (a + b - 1) / b;
 }
 
-template <int E> __device__ __forceinline__ void load_row(const void *base, const uint8_t *scale, size_t row, int lane, int D, float *x)
+// ---- the line of units -----------------------------------------------------------
+
+// Start of CTA c's stretch, and the CTA whose stretch holds unit u, of U units over C CTAs.
+__device__ __forceinline__ int stretch(int c, int U, int C)
 {
-    if (!scale) {
-        const __nv_bfloat16 *p = static_cast<const __nv_bfloat16 *>(base) + row * D + lane * E;
+    return (int)((long long)c * U / C);
+}
+__device__ __forceinline__ int owner(int u, int U, int C)
+{
+    return (int)((((long long)u + 1) * C - 1) / U);
+}
+
+struct Len {
+    int n;
+    bool bad;
+};
+
+__device__ __forceinline__ Len clean_len(const AttnParams &p, int raw)
+{
+    Len r{raw, raw < 0 || raw > p.max_len};
+    if (r.bad)
+        r.n = 0;
+    return r;
+}
+__device__ __forceinline__ int raw_len(const AttnParams &p, int b)
+{
+    return p.max_len > 0 && b < p.B ? __ldg(&p.cache_len[b]) : 0;
+}
+// Tiles of a segment of a sequence with n cached keys; one unit even without any key.
+__device__ __forceinline__ int tiles_of(const AttnParams &p, int n)
+{
+    return max(1, cdiv(n, kTile) + p.has_new);
+}
+
+struct Seg {
+    bool prefix, bad;
+    int b, h;
+    int row0, nrows;  // first row among the head's B*T*G, rows
+    int t0, n, nt;    // tiles t0 .. t0 + n - 1 of nt are this CTA's
+    int keys;         // cached or prefix keys
+    int hn;           // 1: tile 0 is the new tokens'
+    int rb;           // row block within the source
+    int id;           // number among its kind
+    bool first;       // the CTA's first segment
+
+    __device__ bool none() const { return keys == 0 && !hn; }  // a unit without a tile
+    __device__ bool whole() const { return t0 == 0 && n == nt; }
+    __device__ bool draft() const { return hn && t0 == 0; }    // this piece holds the new tokens' tile
+    __device__ bool pair() const { return nrows > kTile; }
+    __device__ int slot_rows(int s) const { return pair() ? min(kTile, nrows - kTile * s) : nrows; }
+    __device__ int key0(int tile) const { return (tile - hn) * kTile; }
+    __device__ int valid(int tile) const { return min(kTile, keys - key0(tile)); }
+};
+
+// Walks the segments of a CTA's stretch; every role walks the same ones.
+struct Walk {
+    int u, u1, b, ub, raw, raw_next;
+    bool first;
+
+    __device__ void start(const AttnParams &p, int u0, int u1_, int b0, int ub0)
+    {
+        u = u0;
+        u1 = u1_;
+        b = b0;
+        ub = ub0;
+        first = true;
+        raw = raw_len(p, b);
+        raw_next = raw_len(p, b + 1);
+    }
+
+    __device__ bool next(const AttnParams &p, Seg &s)
+    {
+        if (u >= u1)
+            return false;
+        s.first = first;
+        first = false;
+        if (u < p.UP) {
+            s.id = u / p.ntp;
+            s.t0 = u - s.id * p.ntp;
+            s.nt = p.ntp;
+            s.n = min(s.nt - s.t0, u1 - u);
+            s.prefix = true;
+            s.bad = false;
+            s.b = 0;
+            s.h = s.id / p.nbp;
+            s.rb = s.id - s.h * p.nbp;
+            s.row0 = s.rb * 2 * kTile;
+            s.nrows = min(2 * kTile, p.B * p.T * p.G - s.row0);
+            s.keys = p.Lp;
+            s.hn = 0;
+            u += s.n;
+            return true;
+        }
+        const Len len = clean_len(p, raw);
+        const int nt = tiles_of(p, len.n), local = u - ub, rel = local / nt;
+        s.prefix = false;
+        s.bad = len.bad;
+        s.b = b;
+        s.h = rel / p.nbs;
+        s.rb = rel - s.h * p.nbs;
+        s.t0 = local - rel * nt;
+        s.nt = nt;
+        s.n = min(nt - s.t0, u1 - u);
+        s.row0 = b * p.T * p.G + s.rb * 2 * kTile;
+        s.nrows = min(2 * kTile, p.T * p.G - s.rb * 2 * kTile);
+        s.keys = len.n;
+        s.hn = p.has_new;
+        s.id = (b * p.H + s.h) * p.nbs + s.rb;
+        u += s.n;
+        if (u == ub + p.H * p.nbs * nt) {
+            ub = u;
+            ++b;
+            raw = raw_next;
+            raw_next = raw_len(p, b + 1);
+        }
+        return true;
+    }
+};
+
+// Ring positions of a segment's tiles: a new tokens' tile (first) and every bf16 tile of D = 128 take two stages.
+template <int D, bool E4> struct Fills {
+    __device__ static bool two(bool draft) { return Cfg<D, E4>::kTwo && (!E4 || draft); }
+    __device__ static uint32_t at(const Seg &s, int i)
+    {
+        if (!Cfg<D, E4>::kTwo)
+            return i;
+        if (!E4)
+            return 2 * i;
+        return i + (s.draft() && i > 0 ? 1 : 0);
+    }
+};
+
+// ---- waits -------------------------------------------------------------------------
+
+// Waits for phase n (counted from 0) of the barrier; after a wait that gave up
+// every later one returns soon, so that each role still ends.
+template <class C> __device__ __forceinline__ void await(C &ctl, uint64_t *bar, uint32_t n)
+{
+    if (*(volatile int *)&ctl.abort || !mbar_wait_bounded(bar, n & 1u, &ctl.abort, kWaitNs))
+        *(volatile int *)&ctl.abort = 1;
+}
+
+__device__ __forceinline__ void bar_sync(int id, int threads)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+__device__ __forceinline__ float nan_f()
+{
+    return __int_as_float(0x7fc00000);
+}
+
+__device__ __forceinline__ unsigned pack_bf16(float lo, float hi)
+{
+    const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const unsigned *>(&r);
+}
+
+// Scale exponent of a magnitude's bf16 bits: smallest e with m <= 448 * 2^e.
+__device__ __forceinline__ int code_exponent(unsigned m)
+{
+    return max((int)(m >> 7) - 127 - 8 + ((m & 127u) > 96u ? 1 : 0), -100);
+}
+
+__device__ __forceinline__ float pow2i(int e)
+{
+    return __int_as_float((e + 127) << 23);
+}
+
+// ---- the kernel ------------------------------------------------------------------------
+
+template <int D, bool E4>
+__global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_constant__ Maps maps, AttnParams p)
+{
+    using C = Cfg<D, E4>;
+    constexpr int kStages = C::kStages;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    unsigned char *ring = smem + 2 * C::kQTile;
+    Ctl<E4> &ctl = *reinterpret_cast<Ctl<E4> *>(ring + kStages * kSlotBytes);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&ctl.full[s], 1);
+            mbar_init(&ctl.empty[s], 2);  // the last MMA's commit and the clearing warp
+            mbar_init(&ctl.fix[s], 1);
+            ctl.last_fill[s] = -1;
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&ctl.s_full[s], 1);
+            mbar_init(&ctl.p_full[s], 4);
+            mbar_init(&ctl.o_full[s], 1);
+        }
+        mbar_init(&ctl.q_full, kSoftmaxThreads);
+        mbar_init(&ctl.poison_full, 1);
+        mbar_init(&ctl.done, 1);
+        ctl.abort = 0;
+        ctl.start_b = 0;
+        ctl.start_ub = p.UP;
+        fence_mbar_init();
+    }
+    if (warp == 9) {
+        tmem_alloc(&ctl.tmem, kTmemCols);
+        tmem_relinquish();
+    }
+    grid_dependency_wait();  // nothing above reads what an earlier kernel wrote
+
+    // ---- units of every sequence: this CTA's stretch and where it starts ----
+    const int per = p.H * p.nbs;  // segments of a sequence
+    const int chunk = cdiv(p.B, kThreads);
+    const int bs = min(p.B, tid * chunk), be = min(p.B, bs + chunk);
+    int mine = 0;
+    for (int b = bs; b < be; ++b)
+        mine += tiles_of(p, clean_len(p, raw_len(p, b)).n);
+    int incl = mine;
 #pragma unroll
-        for (int i = 0; i < E; ++i)
-            x[i] = __bfloat162float(p[i]);
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o)
+            incl += x;
+    }
+    if (lane == 31)
+        ctl.warp_sum[warp] = incl;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    int before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        const int x = ctl.warp_sum[w];
+        before += w < warp ? x : 0;
+        total += x;
+    }
+    const int U = p.UP + per * total;
+    // no more stretches than units: none is empty, the CTAs past them have nothing to do
+    const int nC = min((int)gridDim.x, U);
+    const int u0 = stretch(min((int)blockIdx.x, nC), U, nC), u1 = stretch(min((int)blockIdx.x + 1, nC), U, nC);
+    {
+        int ub = p.UP + per * (before + incl - mine);
+        const int target = max(u0, p.UP);
+        const bool holds = target >= ub && target < ub + per * mine;
+        if (holds || blockIdx.x == 0)
+            for (int b = bs; b < be; ++b) {
+                const int next = ub + per * tiles_of(p, clean_len(p, raw_len(p, b)).n);
+                if (target >= ub && target < next) {
+                    ctl.start_b = b;
+                    ctl.start_ub = ub;
+                }
+                if (blockIdx.x == 0)
+                    p.seg_start[b] = ub;
+                ub = next;
+            }
+        if (blockIdx.x == 0 && tid == 0)
+            p.seg_start[p.B] = U;
+    }
+    __syncthreads();
+    const uint32_t tmem = ctl.tmem;
+    Walk walk;
+    walk.start(p, u0, u1, ctl.start_b, ctl.start_ub);
+    Seg seg;
+
+    if (warp == 8) {
+        // ---- producer ----
+        if (lane == 0) {
+            uint32_t fill = 0;
+            auto acquire = [&](int &s) {
+                s = (int)(fill % kStages);
+                if (fill >= (uint32_t)kStages)
+                    await(ctl, &ctl.empty[s], fill / kStages - 1);
+                return !*(volatile int *)&ctl.abort;
+            };
+            bool ok = true;
+            while (ok && walk.next(p, seg)) {
+                if (seg.none())
+                    continue;
+                for (int i = 0; i < seg.n && ok; ++i) {
+                    const int tile = seg.t0 + i;
+                    const bool draft = seg.hn && tile == 0;
+                    const CUtensorMap *mk = draft ? &maps.kn : seg.prefix ? &maps.kp : &maps.k;
+                    const CUtensorMap *mv = draft ? &maps.vn : seg.prefix ? &maps.vp : &maps.v;
+                    const int key = draft ? 0 : seg.key0(tile), b = seg.prefix ? 0 : seg.b;
+                    int s;
+                    if (Fills<D, E4>::two(draft)) {
+                        for (int half = 0; half < 2 && ok; ++half) {
+                            if (!(ok = acquire(s)))
+                                break;
+                            unsigned char *dst = ring + s * kSlotBytes;
+                            const CUtensorMap *m = half ? mv : mk;
+                            mbar_arrive_expect_tx(&ctl.full[s], 2 * kPanel);
+                            tma_load_4d(dst, m, 0, seg.h, key, b, &ctl.full[s]);
+                            tma_load_4d(dst + kPanel, m, 64, seg.h, key, b, &ctl.full[s]);
+                            ctl.last_fill[s] = (int)fill++;
+                        }
+                    } else {
+                        if (!(ok = acquire(s)))
+                            break;
+                        unsigned char *dst = ring + s * kSlotBytes;
+                        const uint32_t bytes = E4 && !draft ? kTile * D : kPanel;  // of K, of V
+                        mbar_arrive_expect_tx(&ctl.full[s], 2 * bytes);
+                        tma_load_4d(dst, mk, 0, seg.h, key, b, &ctl.full[s]);
+                        tma_load_4d(dst + kVoff, mv, 0, seg.h, key, b, &ctl.full[s]);
+                        ctl.last_fill[s] = (int)fill++;
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 9) {
+        // ---- MMA issuer ----
+        if (lane == 0) {
+            constexpr uint32_t idS = idesc_bf16_f32(kTile, kTile);
+            constexpr uint32_t idO = idesc_bf16_f32(kTile, D) | (1u << 16);
+            constexpr uint32_t idS8 = idesc_f8_f32(0, 0, kTile, kTile, 0);
+            constexpr uint32_t idO8 = idesc_f8_f32(1, 0, kTile, D, 1);
+            constexpr int kSw8 = D;             // an e4m3 row is D bytes: its swizzle
+            constexpr uint32_t kAtom8 = 8 * D;  // 8 rows of it
+            uint32_t base = 0;                  // ring fills before this segment
+            uint32_t nq = 0, npv[2] = {0, 0};
+            while (walk.next(p, seg)) {
+                if (seg.none())
+                    continue;
+                const bool pair = seg.pair(), draft = seg.draft();
+                const int njobs = pair ? 2 * seg.n : seg.n;
+                await(ctl, &ctl.q_full, nq++);
+                tc_fence_after();
+                bool q8 = E4 && !draft;
+                auto scores = [&](int q) {
+                    const int i = pair ? q >> 1 : q, s = q & 1;
+                    const bool dr = draft && i == 0;
+                    if (E4 && !dr && !q8) {
+                        await(ctl, &ctl.q_full, nq++);
+                        tc_fence_after();
+                        q8 = true;
+                    }
+                    const uint32_t f = base + Fills<D, E4>::at(seg, i);
+                    const int st = (int)(f % kStages);
+                    await(ctl, &ctl.full[st], f / kStages);
+                    tc_fence_after();
+                    const unsigned char *qt = smem + (pair ? s : 0) * C::kQTile, *kt = ring + st * kSlotBytes;
+                    const uint32_t d = tmem + 256 + 128 * s;
+                    if (!E4 || dr) {
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk)
+                            tc_mma_bf16(d, smem_desc_k128(qt + kPanel * (kk / 4)) + 2u * (kk & 3),
+                                        smem_desc_k128(kt + kPanel * (kk / 4)) + 2u * (kk & 3), idS, kk != 0);
+                    } else {
+                        const uint64_t dk = smem_desc(kt, 16, kAtom8, kSw8);
+#pragma unroll
+                        for (int part = 0; part < 2; ++part) {
+                            const uint64_t dq = smem_desc(qt + part * (C::kQTile / 2), 16, kAtom8, kSw8);
+#pragma unroll
+                            for (int kk = 0; kk < D / 32; ++kk)
+                                tc_mma_f8(d, dq + 2u * kk, dk + 2u * kk, idS8, part || kk);
+                        }
+                    }
+                    tc_commit(&ctl.s_full[s]);
+                    if (Fills<D, E4>::two(dr) && (!pair || s == 1))
+                        tc_commit(&ctl.empty[st]);  // no later job reads these keys
+                };
+                auto product = [&](int q) {
+                    const int i = pair ? q >> 1 : q, s = q & 1;
+                    const bool dr = draft && i == 0, two = Fills<D, E4>::two(dr);
+                    const uint32_t f = base + Fills<D, E4>::at(seg, i) + (two ? 1 : 0);
+                    const int st = (int)(f % kStages);
+                    await(ctl, &ctl.full[st], f / kStages);
+                    if (dr || (!seg.prefix && seg.valid(seg.t0 + i) < kTile))
+                        await(ctl, &ctl.fix[st], f / kStages);
+                    if (dr && q == 0) {
+                        for (int w = 0; w < 4; ++w)
+                            ctl.poison[w] = ctl.poison_slot[st][w];
+                        mbar_arrive(&ctl.poison_full);
+                    }
+                    await(ctl, &ctl.p_full[s], npv[s]++);
+                    tc_fence_after();
+                    const unsigned char *vt = ring + st * kSlotBytes + (two ? 0 : kVoff);
+                    const uint32_t d = tmem + 128 * s, a = tmem + 256 + 128 * s;
+                    const uint32_t acc = q >= 2;  // the slot's first job of the segment overwrites O
+                    if (!E4 || dr) {
+                        const uint64_t dv = smem_desc(vt, kPanel, 1024, 128);
+#pragma unroll
+                        for (int kk = 0; kk < kTile / 16; ++kk)
+                            tc_mma_bf16_ts(d, a + 8 * kk, dv + (uint32_t)(kk * 16 * 128 / 16), idO, acc | (kk != 0));
+                    } else {
+                        const uint64_t dv = smem_desc(vt, 16, kAtom8, kSw8);
+#pragma unroll
+                        for (int kk = 0; kk < kTile / 32; ++kk)
+#pragma unroll
+                            for (int part = 0; part < 3; ++part)
+                                tc_mma_f8_ts(d, a + 24 * kk + 8 * part, dv + (uint32_t)(kk * 32 * D / 16), idO8,
+                                             acc | (kk != 0) | (part != 0));
+                    }
+                    tc_commit(&ctl.o_full[s]);
+                    if (!pair || s == 1)
+                        tc_commit(&ctl.empty[st]);
+                };
+                scores(0);
+                if (njobs > 1)
+                    scores(1);
+                for (int q = 0; q < njobs; ++q) {
+                    product(q);
+                    if (q + 2 < njobs)
+                        scores(q + 2);
+                }
+                base += Fills<D, E4>::at(seg, seg.n - 1) + (Fills<D, E4>::two(draft && seg.n == 1) ? 2 : 1);
+            }
+            tc_commit(&ctl.done);
+        }
+        __syncwarp();
+    } else if (warp == 10) {
+        // ---- clearing warp: goes over every stage in order, so that a phase is never missed ----
+        uint32_t fill = 0;
+        while (walk.next(p, seg)) {
+            if (seg.none())
+                continue;
+            for (int i = 0; i < seg.n; ++i) {
+                const int tile = seg.t0 + i;
+                const bool draft = seg.hn && tile == 0, two = Fills<D, E4>::two(draft);
+                for (int part = two ? 0 : 1; part < 2; ++part, ++fill) {
+                    const int st = (int)(fill % kStages);
+                    await(ctl, &ctl.full[st], fill / kStages);
+                    if (part == 1) {
+                        unsigned char *vt = ring + st * kSlotBytes + (two ? 0 : kVoff);
+                        if (draft) {
+                            uint32_t bits[4] = {0, 0, 0, 0};
+                            for (int c = lane; c < p.T * (D / 8); c += 32) {  // 16-byte pieces of the tokens' rows
+                                const int row = c / (D / 8), x = c % (D / 8);
+                                uint4 *a = reinterpret_cast<uint4 *>(vt + (x / 8) * kPanel + row * 128 + (x % 8) * 16);
+                                uint4 v = *a;
+                                uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                                bool bad = false;
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    if ((w[k] & 0x7f80u) == 0x7f80u) {
+                                        w[k] &= 0xffff0000u;
+                                        bad = true;
+                                    }
+                                    if ((w[k] & 0x7f800000u) == 0x7f800000u) {
+                                        w[k] &= 0xffffu;
+                                        bad = true;
+                                    }
+                                }
+                                if (bad) {
+                                    *a = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k)
+                                        bits[k] |= (row >> 5) == k ? 1u << (row & 31) : 0u;
+                                }
+                            }
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const uint32_t all = __reduce_or_sync(0xffffffffu, bits[k]);
+                                if (lane == 0)
+                                    ctl.poison_slot[st][k] = all;
+                            }
+                        } else if (!seg.prefix && seg.valid(tile) < kTile) {
+                            // rows behind the length: whatever the cache holds there must not count
+                            constexpr int kRow = E4 ? D : 128, kPanels = E4 ? 1 : D / 64;
+                            const int lo = seg.valid(tile) * kRow;
+                            for (int pn = 0; pn < kPanels; ++pn)
+                                for (int x = lo + lane * 16; x < kTile * kRow; x += 512)
+                                    *reinterpret_cast<uint4 *>(vt + pn * kPanel + x) = make_uint4(0, 0, 0, 0);
+                        }
+                        fence_async_shared();
+                    }
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&ctl.fix[st]);
+                        mbar_arrive(&ctl.empty[st]);
+                    }
+                }
+            }
+        }
     } else {
-        const __nv_fp8_storage_t *p = static_cast<const __nv_fp8_storage_t *>(base) + row * D + lane * E;
-        const float s = code_scale(scale[row]);
+        // ---- softmax and epilogue: slot s, row r ----
+        const int s = warp >> 2, wq = warp & 3, r = wq * 32 + lane;
+        const int pt = tid & 127;  // place in the slot's 128 threads
+        const uint32_t lanes = (uint32_t)(wq * 32) << 16;
+        const uint32_t tS = tmem + lanes + 256 + 128 * s, tO = tmem + lanes + 128 * s;
+        uint32_t nj = 0, npois = 0;  // jobs of the slot, segments with new tokens so far
+        uint32_t ntab = 0;           // e4m3 tiles of the slot so far
+        while (walk.next(p, seg)) {
+            const bool pair = seg.pair(), draft = seg.draft(), none = seg.none();
+            const int njobs = none ? 0 : pair ? 2 * seg.n : seg.n;
+            const int rows = seg.slot_rows(s);
+            const int row0 = seg.row0 + (pair ? kTile * s : 0);
+            const bool active = wq * 32 < rows;  // the warp has rows
+            bool poison = seg.bad;
+            float mu = -INFINITY, l = 0.0f;
+            float cq = p.c;  // factor of an e4m3 job's scores
+            unsigned char *qt = smem + (pair ? s : 0) * C::kQTile;
+            // this thread's 16-byte pieces of Q: rows of its slot's tile, or half of the shared tile's
+            constexpr int kPc = D / 8;                              // pieces of a row
+            const int q_first = pair ? 0 : kTile / 2 * s, q_rows = pair ? kTile : kTile / 2;
+            auto q_piece = [&](int row, int x) {
+                return reinterpret_cast<uint4 *>(qt + (x / 8) * kPanel + row * 128 + (((x & 7) ^ (row & 7)) * 16));
+            };
+            // Q in bf16 -> two e4m3 terms in place; every thread of both slots takes part
+            auto to_codes = [&]() {
+                bar_sync(1, kSoftmaxThreads);  // no product reads Q in bf16 any more, qmax is cleared
+                uint4 x[16];
+                unsigned m = 0;
 #pragma unroll
-        for (int i = 0; i < E; ++i)
-            x[i] = __half2float(__half(__nv_cvt_fp8_to_halfraw(p[i], __NV_E4M3))) * s;
+                for (int k = 0; k < 16; ++k) {
+                    const int e = pt + 128 * k, row = q_first + e / kPc;
+                    if (e < q_rows * kPc) {
+                        x[k] = *q_piece(row, e % kPc);
+                        const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t lo = w[j] & 0x7fffu, hi = (w[j] >> 16) & 0x7fffu;
+                            m = max(m, max(lo >= 0x7f80u ? 0u : lo, hi >= 0x7f80u ? 0u : hi));
+                        }
+                    }
+                }
+                m = __reduce_max_sync(0xffffffffu, m);
+                if (lane == 0)
+                    atomicMax(&ctl.qmax[pair ? s : 0], m);
+                bar_sync(1, kSoftmaxThreads);
+                const int e2 = code_exponent(ctl.qmax[pair ? s : 0]);
+                const float f = pow2i(-e2);
+                cq = p.c * pow2i(e2);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    const int e = pt + 128 * k, row = q_first + e / kPc, x0 = e % kPc;
+                    if (e < q_rows * kPc) {
+                        const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+                        uint32_t hi[2], lo[2];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            float a = __uint_as_float(w[j] << 16), b = __uint_as_float(w[j] & 0xffff0000u);
+                            a = (w[j] & 0x7f80u) == 0x7f80u ? nan_f() : a * f;
+                            b = (w[j] & 0x7f800000u) == 0x7f800000u ? nan_f() : b * f;
+                            const uint32_t ch = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+                            const float2 back = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)ch, __NV_E4M3)));
+                            const uint32_t cl = __nv_cvt_float2_to_fp8x2(make_float2(a - back.x, b - back.y), __NV_SATFINITE, __NV_E4M3);
+                            hi[j >> 1] = (j & 1) ? hi[j >> 1] | (ch << 16) : ch;
+                            lo[j >> 1] = (j & 1) ? lo[j >> 1] | (cl << 16) : cl;
+                        }
+                        // 8 codes at byte 8 * x0 of a D-byte row, 16-byte chunks swizzled as TMA does for rows of D bytes
+                        const int ch16 = x0 >> 1;
+                        const int sw = D == 128 ? ch16 ^ (row & 7) : ch16 ^ ((row >> 1) & 3);
+                        unsigned char *at = qt + row * D + sw * 16 + (x0 & 1) * 8;
+                        *reinterpret_cast<uint2 *>(at) = make_uint2(hi[0], hi[1]);
+                        *reinterpret_cast<uint2 *>(at + C::kQTile / 2) = make_uint2(lo[0], lo[1]);
+                    }
+                }
+                fence_async_shared();
+                mbar_arrive(&ctl.q_full);
+            };
+            uint32_t seen[4] = {0, 0, 0, 0};  // new tokens that this row sees
+            bool convert = false;             // Q has yet to go from bf16 to codes
+            if (!none) {
+                if (E4 && pt == 0)
+                    ctl.qmax[s] = 0;
+#pragma unroll 4
+                for (int k = 0; k < 16; ++k) {
+                    const int e = pt + 128 * k, row = q_first + e / kPc, x = e % kPc;
+                    if (e < q_rows * kPc) {
+                        uint4 v = make_uint4(0, 0, 0, 0);
+                        if (row < rows) {
+                            const int R = row0 + row, tok = R / p.G, b = tok / p.T;
+                            v = __ldg(reinterpret_cast<const uint4 *>(p.q + b * p.q_sb + (long long)(tok - b * p.T) * p.q_st +
+                                                                      (seg.h * p.G + (R - tok * p.G)) * D + x * 8));
+                        }
+                        *q_piece(row, x) = v;
+                    }
+                }
+                if (!E4 || draft) {
+                    fence_async_shared();
+                    mbar_arrive(&ctl.q_full);
+                    convert = E4 && seg.n > 1;
+                } else {
+                    to_codes();
+                }
+                if (draft) {
+                    const int t = min((seg.rb * 2 * kTile + (pair ? kTile * s : 0) + r) / p.G, p.T - 1);
+                    if (p.parent) {
+                        const int32_t *par = p.parent + (long long)seg.b * p.T;
+                        bool bad = false;
+                        for (int k = lane; k < p.T; k += 32) {
+                            const int x = __ldg(&par[k]);
+                            bad |= k == 0 ? x != -1 : x < 0 || x >= k;
+                        }
+                        if (__any_sync(0xffffffffu, bad)) {
+                            poison = true;
+                            if (lane == 0 && p.status && wq == 0 && s == 0)
+                                atomicOr(p.status, SV_ATTN_BAD_TREE);
+                        } else {
+                            for (int j = t; j >= 0; j = __ldg(&par[j]))
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    seen[k] |= (j >> 5) == k ? 1u << (j & 31) : 0u;
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            seen[k] = t - 32 * k >= 31 ? 0xffffffffu : t >= 32 * k ? (2u << (t - 32 * k)) - 1u : 0u;
+                    }
+                }
+                if (convert && s == 1 && !pair) {  // slot 0 alone has the new tokens' job
+                    to_codes();
+                    convert = false;
+                }
+            }
+            // e4m3: the scales of key pt of the slot's next cached tile
+            const int step = pair ? 1 : 2;
+            uint32_t sk = 127, sv_ = 127;
+            auto fetch_scales = [&](int tile) {
+                sk = sv_ = 127;
+                if (E4 && tile < seg.t0 + seg.n) {
+                    const int key = seg.key0(tile) + pt;
+                    if (key >= 0 && key < seg.keys) {
+                        const long long at = ((seg.prefix ? 0ll : (long long)seg.b * p.L) + key) * p.H + seg.h;
+                        sk = __ldg((seg.prefix ? p.kp_scale : p.k_scale) + at);
+                        sv_ = __ldg((seg.prefix ? p.vp_scale : p.v_scale) + at);
+                    }
+                }
+            };
+            const int first_tile = seg.t0 + (pair ? 0 : s);
+            if (E4 && !none)
+                fetch_scales(draft && first_tile == 0 ? first_tile + step : first_tile);
+
+            for (int q = s; q < njobs; q += 2) {
+                const int i = pair ? q >> 1 : q, tile = seg.t0 + i;
+                const bool dr = draft && i == 0;
+                const int valid = dr ? kTile : seg.valid(tile);
+                const float *kk = nullptr, *ev = nullptr, *inv = nullptr;
+                if constexpr (E4) {
+                    if (!dr) {
+                        const int tb = (int)(ntab & 1u);
+                        ctl.tab.kk[s][tb][pt] = cq * __uint_as_float(sk << 23);
+                        ctl.tab.ev[s][tb][pt] = (float)((int)sv_ - 127);
+                        ctl.tab.inv[s][tb][pt] = __uint_as_float((254u - min(sv_, 254u)) << 23);
+                        fetch_scales(tile + step);
+                        ++ntab;
+                        bar_sync(2 + s, 128);
+                        kk = ctl.tab.kk[s][tb];
+                        ev = ctl.tab.ev[s][tb];
+                        inv = ctl.tab.inv[s][tb];
+                    }
+                }
+                await(ctl, &ctl.s_full[s], nj);
+                tc_fence_after();
+                if (E4 && convert) {
+                    to_codes();
+                    convert = false;
+                }
+                if (active) {
+                    // the row's maximum of y over the tile
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int c0 = 0; c0 < kTile; c0 += 32) {
+                        uint32_t x[32];
+                        tmem_ld32_nowait(tS + c0, x);
+                        tmem_wait_ld();
+                        float m0 = -INFINITY, m1 = -INFINITY;
+                        if (valid - c0 < 32 || dr) {
+                            const uint32_t ok = dr ? seen[c0 >> 5] : valid <= c0 ? 0u : valid - c0 >= 32 ? 0xffffffffu : (1u << (valid - c0)) - 1u;
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) {
+                                float y = __uint_as_float(x[k]);
+                                if (E4 && !dr)
+                                    y = fmaf(y, kk[c0 + k], ev[c0 + k]);
+                                m0 = fmaxf(m0, (ok >> k) & 1u ? y : -INFINITY);
+                            }
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 32; k += 2) {
+                                float y0 = __uint_as_float(x[k]), y1 = __uint_as_float(x[k + 1]);
+                                if (E4 && !dr) {
+                                    y0 = fmaf(y0, kk[c0 + k], ev[c0 + k]);
+                                    y1 = fmaf(y1, kk[c0 + k + 1], ev[c0 + k + 1]);
+                                }
+                                m0 = fmaxf(m0, y0);
+                                m1 = fmaxf(m1, y1);
+                            }
+                        }
+                        mx = fmaxf(mx, fmaxf(m0, m1));
+                    }
+                    if (!E4 || dr)
+                        mx *= p.c;
+                    const bool grow = mx > mu + C::kSlack || (mu == -INFINITY && mx > mu);
+                    if (__any_sync(0xffffffffu, grow)) {
+                        const float mn = fmaxf(mu, mx);
+                        const float f = mu == -INFINITY ? 0.0f : ex2(mu - mn);
+                        mu = mn;
+                        l *= f;
+                        if (q >= 2) {  // O holds earlier tiles: their product must be complete
+                            await(ctl, &ctl.o_full[s], nj - 1);
+                            tc_fence_after();
+#pragma unroll
+                            for (int c0 = 0; c0 < D; c0 += 32) {
+                                uint32_t x[32];
+                                tmem_ld32_nowait(tO + c0, x);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int k = 0; k < 32; ++k)
+                                    x[k] = f == 0.0f ? 0u : __float_as_uint(__uint_as_float(x[k]) * f);
+                                tmem_st32(tO + c0, x);
+                            }
+                        }
+                    }
+                    const float R = mu == -INFINITY ? 0.0f : mu - C::kBase;
+                    float l0 = 0.0f, l1 = 0.0f;
+#pragma unroll
+                    for (int c0 = 0; c0 < kTile; c0 += 32) {
+                        uint32_t x[32];
+                        tmem_ld32_nowait(tS + c0, x);
+                        tmem_wait_ld();
+                        if (valid - c0 < 32 || dr) {
+                            const uint32_t ok = dr ? seen[c0 >> 5] : valid <= c0 ? 0u : valid - c0 >= 32 ? 0xffffffffu : (1u << (valid - c0)) - 1u;
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                x[k] = (ok >> k) & 1u ? x[k] : 0xff800000u;
+                        }
+                        if (!E4 || dr) {
+#pragma unroll
+                            for (int k = 0; k < 32; k += 2) {
+                                const float w0 = ex2(fmaf(__uint_as_float(x[k]), p.c, -R));
+                                const float w1 = ex2(fmaf(__uint_as_float(x[k + 1]), p.c, -R));
+                                l0 += w0;
+                                l1 += w1;
+                                x[k >> 1] = pack_bf16(w0, w1);
+                            }
+                            tmem_st16(tS + (c0 >> 1), x);
+                        } else {
+                            uint32_t w24[24];
+#pragma unroll
+                            for (int k = 0; k < 32; k += 4) {
+                                float w[4];
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) {
+                                    w[j] = ex2(fmaf(__uint_as_float(x[k + j]), kk[c0 + k + j], ev[c0 + k + j]) - R);
+                                    if (j & 1)
+                                        l1 = fmaf(w[j], inv[c0 + k + j], l1);
+                                    else
+                                        l0 = fmaf(w[j], inv[c0 + k + j], l0);
+                                }
+                                // three e5m2 terms of f16 weights: the upper bytes of w, of w - first, of the rest
+                                __half2 a = __floats2half2_rn(w[0], w[1]), b = __floats2half2_rn(w[2], w[3]);
+#pragma unroll
+                                for (int part = 0; part < 2; ++part) {
+                                    const uint32_t ua = *reinterpret_cast<uint32_t *>(&a), ub = *reinterpret_cast<uint32_t *>(&b);
+                                    w24[part * 8 + (k >> 2)] = __byte_perm(ua, ub, 0x7531);
+                                    const uint32_t ta = ua & 0xff00ff00u, tb = ub & 0xff00ff00u;
+                                    a = __hsub2(a, *reinterpret_cast<const __half2 *>(&ta));
+                                    b = __hsub2(b, *reinterpret_cast<const __half2 *>(&tb));
+                                }
+                                const uint32_t la = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(a), __NV_SATFINITE, __NV_E5M2);
+                                const uint32_t lb = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(b), __NV_SATFINITE, __NV_E5M2);
+                                w24[16 + (k >> 2)] = la | (lb << 16);
+                            }
+                            const uint32_t at = tS + (c0 >> 5) * 24;
+                            tmem_st16(at, w24);
+                            tmem_st8(at + 16, w24 + 16);
+                        }
+                    }
+                    l += l0 + l1;
+                    tmem_wait_st();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&ctl.p_full[s]);
+                ++nj;
+            }
+
+            // ---- epilogue: join the slots, write ----
+            const bool has = s < njobs, other = (1 - s) < njobs;
+            if (has)
+                await(ctl, &ctl.o_full[s], nj - 1);
+            if (draft) {
+                await(ctl, &ctl.poison_full, npois++);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    poison |= (seen[k] & ctl.poison[k]) != 0;
+            }
+            tc_fence_after();
+            if (poison)
+                l = nan_f();
+            float f_own = mu == -INFINITY ? 0.0f : 1.0f, f_oth = 0.0f;
+            if (!pair) {
+                bar_sync(1, kSoftmaxThreads);  // all of both slots' products are complete, Q is free
+                float2 *xch = reinterpret_cast<float2 *>(smem);
+                xch[s * kTile + r] = make_float2(mu, l);
+                bar_sync(1, kSoftmaxThreads);
+                const float2 o = xch[(1 - s) * kTile + r];
+                const float mn = fmaxf(mu, o.x);
+                f_own = mu == -INFINITY ? 0.0f : ex2(mu - mn);
+                f_oth = o.x == -INFINITY ? 0.0f : ex2(o.x - mn);
+                // NaN is kept whatever the factor
+                l = (l != l ? l : l * f_own) + (o.y != o.y ? o.y : o.y * f_oth);
+                mu = mn;
+            }
+            if (seg.bad && p.status && tid == 0)
+                atomicOr(p.status, SV_ATTN_BAD_LEN);
+            if (active) {
+                const float R = mu - C::kBase;  // -inf when nothing was seen
+                const bool valid_row = r < rows;
+                const bool direct = p.UP == 0 && seg.whole();
+                const int cs = pair ? 0 : s * (D / 2), ce = pair ? D : cs + D / 2;
+                float *part = nullptr;
+                if (!direct) {
+                    const int rr = r + (pair ? kTile * s : 0);
+                    float *slot;
+                    int nr;
+                    if (!seg.whole()) {
+                        nr = p.rm;
+                        slot = p.pieces + (size_t)(2 * blockIdx.x + (seg.first ? 0 : 1)) * nr * (D + 4);
+                    } else {
+                        nr = seg.prefix ? p.rp : p.rs;
+                        slot = (seg.prefix ? p.whole_p : p.whole_s) + (size_t)seg.id * nr * (D + 4);
+                    }
+                    part = slot + (size_t)rr * D;
+                    if (valid_row && (pair || s == 0))
+                        *reinterpret_cast<float2 *>(slot + (size_t)nr * D + rr * 2) = make_float2(R, l);
+                }
+                const float scl = direct ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
+                const int Rg = row0 + r, tok = Rg / p.G;
+                const size_t orow = (size_t)tok * p.Hq + seg.h * p.G + (Rg - tok * p.G);
+                f_own *= scl;
+                f_oth *= scl;
+#pragma unroll 1
+                for (int c0 = cs; c0 < ce; c0 += 32) {
+                    uint32_t x[32];
+                    float o[32];
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        o[k] = scl != scl ? scl : 0.0f;
+                    if (has) {
+                        tmem_ld32_nowait(tO + c0, x);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            o[k] += f_own == 0.0f ? 0.0f : f_own * __uint_as_float(x[k]);
+                    }
+                    if (!pair && other) {
+                        tmem_ld32_nowait((s ? tO - 128 : tO + 128) + c0, x);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            o[k] += f_oth == 0.0f ? 0.0f : f_oth * __uint_as_float(x[k]);
+                    }
+                    if (valid_row) {
+                        if (direct) {
+                            uint4 *dst = reinterpret_cast<uint4 *>(p.out + orow * D + c0);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                dst[k] = make_uint4(pack_bf16(o[8 * k], o[8 * k + 1]), pack_bf16(o[8 * k + 2], o[8 * k + 3]),
+                                                    pack_bf16(o[8 * k + 4], o[8 * k + 5]), pack_bf16(o[8 * k + 6], o[8 * k + 7]));
+                        } else {
+                            float4 *dst = reinterpret_cast<float4 *>(part + c0);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                        }
+                    }
+                }
+                if (direct && valid_row && p.lse && (pair || s == 0))
+                    p.lse[orow] = l == 0.0f ? -INFINITY : (R + log2f(l)) * 0.69314718055994531f;
+            }
+            tc_fence_before();
+            bar_sync(1, kSoftmaxThreads);  // O has been read by both slots, Q and the exchange may be overwritten
+            tc_fence_after();
+        }
     }
+    tc_fence_before();
+    __syncthreads();
+    if (ctl.abort) {
+        // let what is in flight end before the CTA's memory goes
+        if (tid == 0) {
+            int never = 0;
+            for (int s = 0; s < kStages; ++s)
+                if (ctl.last_fill[s] >= 0)
+                    mbar_wait_bounded(&ctl.full[s], (uint32_t)(ctl.last_fill[s] / kStages) & 1u, &never, kWaitNs / 4);
+            mbar_wait_bounded(&ctl.done, 0, &never, kWaitNs / 4);
+            if (p.status)
+                atomicOr(p.status, SV_ATTN_TIMEOUT);
+        }
+        __syncthreads();
+    }
+    tc_fence_after();
+    if (warp == 9)
+        tmem_dealloc(tmem, kTmemCols);
 }
 
-// One warp per query row, one pass over the keys with the running maximum and sum.
-template <int E> __global__ void __launch_bounds__(128) sv_attention_kernel(Params p)
+// ---- joining the parts of cut rows -----------------------------------------------------
+
+// W warps per row (W = 8: a row's parts are dealt to the warps).
+template <int D, int W> __global__ void __launch_bounds__(256) sv_attention_join_kernel(AttnParams p, int grid)
 {
-    const sv_attention_args &a = p.a;
-    const int lane = threadIdx.x & 31;
-    const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int T = (int)a.T, Hq = (int)a.heads_q, Hk = (int)a.heads_kv, D = 32 * E;
-    if (row >= a.B * T * Hq)
+    constexpr int E = D / 32;  // columns of a lane
+    __shared__ float sh[W == 1 ? 1 : W * (D + 2)];
+    grid_dependency_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long row = W == 1 ? (long long)blockIdx.x * 8 + warp : blockIdx.x;
+    if (row >= (long long)p.B * p.T * p.Hq)
         return;
-    const int hq = (int)(row % Hq), t = (int)(row / Hq % T);
-    const long long b = row / Hq / T;
-    const int h = hq / (Hq / Hk);
-    float q[E], o[E], m = -INFINITY, l = 0.0f;
-    bool poison = false;
-    const __nv_bfloat16 *qp = static_cast<const __nv_bfloat16 *>(a.q) + b * a.q_stride_b + t * a.q_stride_t + hq * D + lane * E;
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-        q[i] = __bfloat162float(qp[i]);
-        o[i] = 0.0f;
+    const int hq = (int)(row % p.Hq), tok = (int)(row / p.Hq), b = tok / p.T, h = hq / p.G;
+    const int R = tok * p.G + (hq - h * p.G), local = R - b * p.T * p.G;
+    const int U = __ldg(&p.seg_start[p.B]), ub = __ldg(&p.seg_start[b]), ue = __ldg(&p.seg_start[b + 1]);
+    const int C = min(grid, U);
+    const int nt = (ue - ub) / (p.H * p.nbs);
+    const int rb = local / (2 * kTile), id_s = (b * p.H + h) * p.nbs + rb;
+    const int us = ub + (h * p.nbs + rb) * nt;
+    const int s0 = owner(us, U, C), s1 = owner(us + nt - 1, U, C);
+    if (p.UP == 0 && s0 == s1)
+        return;  // written directly
+    int id_p = 0, up = 0, p0 = 0, p1 = -1;
+    if (p.UP > 0) {
+        id_p = h * p.nbp + R / (2 * kTile);
+        up = id_p * p.ntp;
+        p0 = owner(up, U, C);
+        p1 = owner(up + p.ntp - 1, U, C);
     }
-    const float c = (float)(a.softmax_scale * 1.4426950408889634);
-    auto step = [&](const float *k, const float *v) {
-        float s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < E; ++i)
-            s = fmaf(q[i], k[i], s);
-#pragma unroll
-        for (int d = 16; d >= 1; d >>= 1)
-            s += __shfl_xor_sync(0xffffffffu, s, d);
-        s *= c;
-        const float mn = fmax_nan(m, s), mu = mn == -INFINITY ? 0.0f : mn;
-        const float f = exp2f(m - mu), w = exp2f(s - mu);
-        l = l * f + w;
-#pragma unroll
-        for (int i = 0; i < E; ++i)
-            o[i] = fmaf(w, v[i], o[i] * f);
-        m = mn;
+    const int np = p1 - p0 + 1, n = np + (s1 - s0 + 1);
+    // part i: its row of O, and (R, l)
+    auto part = [&](int i, const float *&o) {
+        const float *slot;
+        int nr, rr;
+        if (i < np) {
+            rr = R % (2 * kTile);
+            if (np == 1) {
+                nr = p.rp;
+                slot = p.whole_p + (size_t)id_p * nr * (D + 4);
+            } else {
+                nr = p.rm;
+                slot = p.pieces + (size_t)(2 * (p0 + i) + (stretch(p0 + i, U, C) >= up ? 0 : 1)) * nr * (D + 4);
+            }
+        } else {
+            rr = local % (2 * kTile);
+            if (s0 == s1) {
+                nr = p.rs;
+                slot = p.whole_s + (size_t)id_s * nr * (D + 4);
+            } else {
+                const int c = s0 + i - np;
+                nr = p.rm;
+                slot = p.pieces + (size_t)(2 * c + (stretch(c, U, C) >= us ? 0 : 1)) * nr * (D + 4);
+            }
+        }
+        o = slot + (size_t)rr * D;
+        return *reinterpret_cast<const float2 *>(slot + (size_t)nr * D + rr * 2);
     };
-    float k[E], v[E];
-    const bool e4 = a.format == SV_KV_E4M3;
-    for (long long j = 0; j < a.prefix_len; ++j) {
-        const size_t r = (size_t)j * Hk + h;
-        load_row<E>(a.k_prefix, e4 ? a.k_prefix_scale : nullptr, r, lane, D, k);
-        load_row<E>(a.v_prefix, e4 ? a.v_prefix_scale : nullptr, r, lane, D, v);
-        step(k, v);
-    }
-    long long len = a.max_len > 0 ? a.cache_len[b] : 0;
-    if (len < 0 || len > a.max_len) {
-        if (lane == 0 && a.status)
-            atomicOr(a.status, SV_ATTN_BAD_LEN);
-        len = 0;
-        poison = true;
-    }
-    for (long long j = 0; j < len; ++j) {
-        const size_t r = ((size_t)b * a.max_len + j) * Hk + h;
-        load_row<E>(a.k_cache, e4 ? a.k_scale : nullptr, r, lane, D, k);
-        load_row<E>(a.v_cache, e4 ? a.v_scale : nullptr, r, lane, D, v);
-        step(k, v);
-    }
-    if (a.k_new) {
-        const int32_t *par = a.parent ? a.parent + b * T : nullptr;
-        if (par) {
-            bool bad = false;
-            for (int n = lane; n < T; n += 32)
-                bad |= n == 0 ? par[n] != -1 : par[n] < 0 || par[n] >= n;
-            if (__any_sync(0xffffffffu, bad)) {
-                if (lane == 0 && a.status)
-                    atomicOr(a.status, SV_ATTN_BAD_TREE);
-                poison = true;
-            }
-        }
-        for (int j = t; j >= 0 && !poison; j = par ? par[j] : j - 1) {
-            const __nv_bfloat16 *kp = static_cast<const __nv_bfloat16 *>(a.k_new) + b * a.new_stride_b + j * a.new_stride_t + h * D + lane * E;
-            const __nv_bfloat16 *vp = static_cast<const __nv_bfloat16 *>(a.v_new) + b * a.new_stride_b + j * a.new_stride_t + h * D + lane * E;
-            bool nf = false;
+    const float *op;
+    float top = -INFINITY;
+    for (int i = lane; i < n; i += 32)
+        top = fmaxf(top, part(i, op).x);
 #pragma unroll
-            for (int i = 0; i < E; ++i) {
-                k[i] = __bfloat162float(kp[i]);
-                v[i] = __bfloat162float(vp[i]);
-                nf |= !isfinite(v[i]);
-            }
-            if (__any_sync(0xffffffffu, nf))
-                l = __int_as_float(0x7fc00000);
-            step(k, v);
+    for (int d = 16; d >= 1; d >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    float acc[E], l = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        acc[e] = 0.0f;
+#pragma unroll 4
+    for (int i = W == 1 ? 0 : warp; i < n; i += W) {
+        const float2 m = part(i, op);
+        const float f = m.x == -INFINITY ? 0.0f : ex2(m.x - top);
+        l += m.y != m.y ? m.y : f * m.y;
+        float o[E];
+        if constexpr (E == 4)
+            *reinterpret_cast<float4 *>(o) = *reinterpret_cast<const float4 *>(op + lane * 4);
+        else
+            *reinterpret_cast<float2 *>(o) = *reinterpret_cast<const float2 *>(op + lane * 2);
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            acc[e] += f == 0.0f ? 0.0f : f * o[e];
+    }
+    if constexpr (W > 1) {
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            sh[warp * (D + 2) + lane * E + e] = acc[e];
+        if (lane == 0)
+            sh[warp * (D + 2) + D] = l;
+        __syncthreads();
+        if (warp != 0)
+            return;
+        for (int w = 1; w < W; ++w) {
+            l += sh[w * (D + 2) + D];
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                acc[e] += sh[w * (D + 2) + lane * E + e];
         }
     }
-    const bool empty = m == -INFINITY && l == 0.0f;
-    const float nan = __int_as_float(0x7fc00000);
-    const float inv = poison ? nan : empty ? 0.0f : 1.0f / l;
-    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + row * D + lane * E;
-#pragma unroll
-    for (int i = 0; i < E; ++i)
-        out[i] = __float2bfloat16(o[i] * inv);
-    if (a.lse && lane == 0)
-        a.lse[row] = poison ? nan : (m + log2f(l)) * 0.69314718055994531f;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    __nv_bfloat16 *dst = p.out + row * D + lane * E;
+    if constexpr (E == 4)
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
+    else
+        *reinterpret_cast<unsigned *>(dst) = pack_bf16(acc[0] * inv, acc[1] * inv);
+    if (p.lse && lane == 0)
+        p.lse[row] = l == 0.0f ? -INFINITY : (top + log2f(l)) * 0.69314718055994531f;
+}
+
+// ---- host side -------------------------------------------------------------------------
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn()
+{
+    static std::atomic<EncodeTiledFn> fn{nullptr};
+    EncodeTiledFn f = fn.load();
+    if (!f) {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) !=
+                cudaSuccess ||
+            q != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            return nullptr;
+        }
+        f = reinterpret_cast<EncodeTiledFn>(ptr);
+        fn.store(f);
+    }
+    return f;
+}
+
+// [B][n][heads][D] (strides in elements) as a map with boxes of 128 keys of one head: 64 bf16 or D codes wide.
+bool make_map(CUtensorMap *m, const void *base, bool codes, int64_t B, int64_t n, int64_t heads, int64_t D, int64_t sb,
+              int64_t sn)
+{
+    EncodeTiledFn enc = encode_fn();
+    if (!enc)
+        return false;
+    const cuuint64_t es = codes ? 1 : 2;
+    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)n, (cuuint64_t)B};
+    const cuuint64_t strides[3] = {(cuuint64_t)D * es, (cuuint64_t)sn * es, (cuuint64_t)sb * es};
+    const cuuint32_t box[4] = {(cuuint32_t)(codes ? D : 64), 1, kTile, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(m, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base),
+               dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               codes && D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 sv_status check(const sv_attention_args *a)
@@ -148,14 +1201,112 @@ sv_status check(const sv_attention_args *a)
         return SV_ERR_SHAPE;
     if (a->format != SV_KV_BF16 && a->format != SV_KV_E4M3)
         return SV_ERR_DTYPE;
-    if (!(a->softmax_scale > 0.0) || !std::isfinite((float)a->softmax_scale) || !((float)a->softmax_scale > 0.0f))
+    const float sc = (float)a->softmax_scale, c = (float)(a->softmax_scale * 1.4426950408889634);
+    if (!(sc >= 1e-30f) || !std::isfinite(c))
         return SV_ERR_INVALID_ARG;
     return SV_OK;
+}
+
+// Sizes of a call, false when they pass the 32-bit counts of the kernels.
+struct Plan {
+    int G, nbp, ntp, nbs, rp, rs, rm;
+    int64_t UP, most;  // prefix units, units at full lengths
+    int64_t off_wp, off_ws, off_pc, bytes;
+};
+
+bool plan(const sv_attention_args &a, Plan &w)
+{
+    const int64_t big = INT_MAX;
+    if (a.heads_q > big / 4 || a.max_len > big - 256 || a.prefix_len > big - 256 || a.B > big / a.T / a.heads_q)
+        return false;
+    w.G = (int)(a.heads_q / a.heads_kv);
+    const int64_t rows = a.B * a.T * w.G, seq_rows = a.T * w.G;
+    w.ntp = (int)((a.prefix_len + kTile - 1) / kTile);
+    w.nbp = (int)((rows + 2 * kTile - 1) / (2 * kTile));
+    w.nbs = (int)((seq_rows + 2 * kTile - 1) / (2 * kTile));
+    w.UP = a.heads_kv * w.nbp * w.ntp;  // below 2^31 * 2^24
+    const int64_t tiles = (a.max_len + kTile - 1) / kTile + 1;
+    if (w.UP > big / 2 || a.heads_kv * w.nbs > big || a.B * a.heads_kv * w.nbs > big || tiles > big / 2 / (a.B * a.heads_kv * w.nbs + 1))
+        return false;
+    w.most = w.UP + a.B * a.heads_kv * w.nbs * tiles;
+    w.rp = (int)(rows < 2 * kTile ? rows : 2 * kTile);
+    w.rs = (int)(seq_rows < 2 * kTile ? seq_rows : 2 * kTile);
+    w.rm = a.prefix_len > 0 ? w.rp : w.rs;
+    const int64_t per = (a.head_dim + 4) * 4;
+    int64_t at = ((a.B + 1) * 4 + 1023) / 1024 * 1024;
+    w.off_wp = at;
+    at += a.prefix_len > 0 ? a.heads_kv * w.nbp * w.rp * per : 0;
+    at = (at + 1023) / 1024 * 1024;
+    w.off_ws = at;
+    at += a.prefix_len > 0 ? a.B * a.heads_kv * w.nbs * w.rs * per : 0;
+    at = (at + 1023) / 1024 * 1024;
+    w.off_pc = at;
+    at += (int64_t)2 * kMaxCtas * w.rm * per;
+    w.bytes = at;
+    return true;
 }
 
 bool al16(const void *p)
 {
     return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
+}
+
+template <int D, bool E4> cudaError_t set_attr()
+{
+    return cudaFuncSetAttribute(sv_attention_kernel<D, E4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)smem_bytes<D, E4>());
+}
+
+// Function attributes and the SM count, once per device.
+constexpr int kMaxDev = 64;
+int device_sms()
+{
+    static std::atomic<int> sms[kMaxDev];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) {
+        cudaGetLastError();
+        return 0;
+    }
+    int n = sms[dev].load();
+    if (n > 0)
+        return n;
+    if (set_attr<64, false>() != cudaSuccess || set_attr<64, true>() != cudaSuccess || set_attr<128, false>() != cudaSuccess ||
+        set_attr<128, true>() != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) {
+        cudaGetLastError();
+        return 0;
+    }
+    sms[dev].store(n);
+    return n;
+}
+
+template <int D, bool E4> sv_status launch(const Maps &maps, const AttnParams &p, int C, cudaStream_t st)
+{
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)C);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem_bytes<D, E4>();
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, sv_attention_kernel<D, E4>, maps, p);
+    if (e == cudaSuccess) {
+        // few rows: a CTA joins one row, its parts dealt to the warps
+        const long long rows = (long long)p.B * p.T * p.Hq;
+        const bool wide = rows <= 1024;
+        cfg.gridDim = dim3((unsigned)(wide ? rows : (rows + 7) / 8));
+        cfg.blockDim = dim3(256);
+        cfg.dynamicSmemBytes = 0;
+        e = wide ? cudaLaunchKernelEx(&cfg, sv_attention_join_kernel<D, 8>, p, C)
+                 : cudaLaunchKernelEx(&cfg, sv_attention_join_kernel<D, 1>, p, C);
+    }
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return SV_ERR_CUDA;
+    }
+    return SV_OK;
 }
 
 } // namespace
@@ -167,7 +1318,10 @@ extern "C" sv_status spec_verify_attention_workspace(const sv_attention_args *ar
         return st;
     if (!bytes)
         return SV_ERR_INVALID_ARG;
-    *bytes = 16;
+    Plan w;
+    if (!plan(*args, w))
+        return SV_ERR_TOO_LARGE;
+    *bytes = w.bytes;
     return SV_OK;
 }
 
@@ -179,30 +1333,93 @@ extern "C" sv_status spec_verify_attention(const sv_attention_args *args, void *
     const sv_attention_args &a = *args;
     if (a.B == 0)
         return SV_OK;
-    const bool e4 = a.format == SV_KV_E4M3;
-    if (!a.q || !a.out || (a.max_len > 0 && (!a.k_cache || !a.v_cache || !a.cache_len || (e4 && (!a.k_scale || !a.v_scale)))) ||
-        (a.prefix_len > 0 && (!a.k_prefix || !a.v_prefix || (e4 && (!a.k_prefix_scale || !a.v_prefix_scale)))) ||
-        (!a.k_new) != (!a.v_new))
+    const bool e4 = a.format == SV_KV_E4M3, has_new = a.k_new != nullptr;
+    if (!a.q || !a.out || (!a.k_new) != (!a.v_new) ||
+        (a.max_len > 0 && (!a.k_cache || !a.v_cache || !a.cache_len || (e4 && (!a.k_scale || !a.v_scale)))) ||
+        (a.prefix_len > 0 && (!a.k_prefix || !a.v_prefix || (e4 && (!a.k_prefix_scale || !a.v_prefix_scale)))))
         return SV_ERR_INVALID_ARG;
     if (!al16(a.q) || !al16(a.out) || !al16(a.k_cache) || !al16(a.v_cache) || !al16(a.k_prefix) || !al16(a.v_prefix) ||
         !al16(a.k_new) || !al16(a.v_new) || !al16(a.workspace))
         return SV_ERR_INVALID_ARG;
     const int64_t qrow = a.heads_q * a.head_dim, nrow = a.heads_kv * a.head_dim;
-    if ((a.B > 1 && a.q_stride_b < qrow) || (a.T > 1 && a.q_stride_t < qrow) ||
-        (a.k_new && ((a.B > 1 && a.new_stride_b < nrow) || (a.T > 1 && a.new_stride_t < nrow))))
+    if ((a.B > 1 && (a.q_stride_b < qrow || a.q_stride_b % 8)) || (a.T > 1 && (a.q_stride_t < qrow || a.q_stride_t % 8)))
         return SV_ERR_INVALID_ARG;
-    if (!a.workspace || a.workspace_bytes < 16)
+    if (has_new && ((a.B > 1 && (a.new_stride_b < nrow || a.new_stride_b % 8)) ||
+                    (a.T > 1 && (a.new_stride_t < nrow || a.new_stride_t % 8))))
         return SV_ERR_INVALID_ARG;
-    if (a.q_stride_b % 8 || a.q_stride_t % 8 || (a.k_new && (a.new_stride_b % 8 || a.new_stride_t % 8)))
-        return SV_ERR_INVALID_ARG;
-    if (a.B > INT_MAX / a.T / a.heads_q || a.B * ((a.max_len + 127) / 128 + 1) > INT_MAX / a.heads_kv)
+    Plan w;
+    // the tensor maps take strides below 2^40 bytes
+    if (!plan(a, w) || a.max_len > (1ll << 38) / nrow || (a.B > 1 && a.new_stride_b > (1ll << 38)) ||
+        (a.T > 1 && a.new_stride_t > (1ll << 38)))
         return SV_ERR_TOO_LARGE;
-    Params p{a};
-    const unsigned grid = (unsigned)((a.B * a.T * a.heads_q + 3) / 4);
+    if (!a.workspace || a.workspace_bytes < w.bytes)
+        return SV_ERR_INVALID_ARG;
+    const int sms = device_sms();
+    if (sms == 0)
+        return SV_ERR_CUDA;
+
+    Maps maps;
+    const int D = (int)a.head_dim;
+    bool any = false, ok = true;
+    auto map = [&](CUtensorMap *m, const void *base, bool codes, int64_t B, int64_t n, int64_t sb, int64_t sn) {
+        ok = ok && make_map(m, base, codes, B, n, a.heads_kv, D, sb, sn);
+        any = true;
+    };
+    if (a.max_len > 0) {
+        map(&maps.k, a.k_cache, e4, a.B, a.max_len, a.max_len * nrow, nrow);
+        map(&maps.v, a.v_cache, e4, a.B, a.max_len, a.max_len * nrow, nrow);
+    }
+    if (has_new) {
+        const int64_t sn = a.T > 1 ? a.new_stride_t : nrow, sb = a.B > 1 ? a.new_stride_b : a.T * sn;
+        map(&maps.kn, a.k_new, false, a.B, a.T, sb, sn);
+        map(&maps.vn, a.v_new, false, a.B, a.T, sb, sn);
+    }
+    if (a.prefix_len > 0) {
+        map(&maps.kp, a.k_prefix, e4, 1, a.prefix_len, a.prefix_len * nrow, nrow);
+        map(&maps.vp, a.v_prefix, e4, 1, a.prefix_len, a.prefix_len * nrow, nrow);
+    }
+    if (!ok)
+        return SV_ERR_CUDA;
+
+    AttnParams p = {};
+    p.q = static_cast<const __nv_bfloat16 *>(a.q);
+    p.k_scale = a.k_scale;
+    p.v_scale = a.v_scale;
+    p.kp_scale = a.k_prefix_scale;
+    p.vp_scale = a.v_prefix_scale;
+    p.cache_len = a.cache_len;
+    p.parent = has_new ? a.parent : nullptr;
+    p.out = static_cast<__nv_bfloat16 *>(a.out);
+    p.lse = a.lse;
+    p.status = a.status;
+    unsigned char *ws = static_cast<unsigned char *>(a.workspace);
+    p.seg_start = reinterpret_cast<int32_t *>(ws);
+    p.whole_p = reinterpret_cast<float *>(ws + w.off_wp);
+    p.whole_s = reinterpret_cast<float *>(ws + w.off_ws);
+    p.pieces = reinterpret_cast<float *>(ws + w.off_pc);
+    p.q_sb = a.q_stride_b;
+    p.q_st = a.q_stride_t;
+    p.B = (int)a.B;
+    p.T = (int)a.T;
+    p.Hq = (int)a.heads_q;
+    p.H = (int)a.heads_kv;
+    p.G = w.G;
+    p.L = p.max_len = (int)a.max_len;
+    p.Lp = (int)a.prefix_len;
+    p.has_new = has_new ? 1 : 0;
+    p.nbp = w.nbp;
+    p.ntp = w.ntp;
+    p.UP = (int)w.UP;
+    p.nbs = w.nbs;
+    p.rp = w.rp;
+    p.rs = w.rs;
+    p.rm = w.rm;
+    p.c = (float)(a.softmax_scale * 1.4426950408889634);
+    int C = sms < kMaxCtas ? sms : kMaxCtas;
+    if (w.most < C)
+        C = (int)w.most;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (a.head_dim == 64)
-        sv_attention_kernel<2><<<grid, 128, 0, s>>>(p);
-    else
-        sv_attention_kernel<4><<<grid, 128, 0, s>>>(p);
-    return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+    if (D == 64)
+        return e4 ? launch<64, true>(maps, p, C, s) : launch<64, false>(maps, p, C, s);
+    return e4 ? launch<128, true>(maps, p, C, s) : launch<128, false>(maps, p, C, s);
 }

@@ -60,6 +60,7 @@
 #include <atomic>
 #include <climits>
 #include <cmath>
+#include <cstddef>
 #include <cstdint>
 #include <mutex>
 
@@ -76,10 +77,16 @@ constexpr int kSlotBytes = 32768;     // one ring stage
 constexpr int kVoff = 16384;          // V's place in a stage that holds K and V
 constexpr int kPanel = kTile * 128;   // 128 rows of 128 bytes
 constexpr int kSoftmaxThreads = 256;
-constexpr int kThreads = 352;
+constexpr int kThreads = 384;          // warp 11 idles: registers are moved by groups of four warps
+// 384 threads start with 168 registers each; 256 softmax threads take 216, the
+// other 128 keep 72: the same 64512 in all
+constexpr int kRegsStart = 168, kRegsSoftmax = 216, kRegsOther = 72;
+static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * kRegsStart, "the split is covered by what the launch holds");
+constexpr int kSegCost = 1;           // what a segment costs beside its tiles, in tiles
 constexpr int kMaxCtas = 160;         // of the grid; the workspace counts on it
 constexpr uint32_t kTmemCols = 512;
 constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr uint32_t kHintNs = 100000;
 constexpr int kMaxStages = 6;
 
 template <int D, bool E4> struct Cfg {
@@ -103,6 +110,7 @@ struct AttnParams {
     long long q_sb, q_st;
     int B, T, Hq, H, G, L, Lp;
     int has_new, max_len;
+    int tma_q;              // a sequence's rows fit one slot: their queries come by TMA
     int nbp, ntp, UP;       // prefix: row blocks and tiles a head, units in all
     int nbs;                // row blocks of a sequence's rows
     int rp, rs, rm;         // rows of a slot in whole_p, whole_s, pieces
@@ -110,11 +118,11 @@ struct AttnParams {
 };
 
 struct Maps {
-    CUtensorMap k, v, kn, vn, kp, vp;
+    CUtensorMap k, v, kn, vn, kp, vp, q;
 };
 
 template <bool E4> struct Tables {};
-template <> struct Tables<true> {
+template <> struct alignas(16) Tables<true> {  // read four keys at a time
     float kk[2][2][kTile];   // per slot, alternating: the key's factor of S
     float ev[2][2][kTile];   // exponent of the value's scale
     float inv[2][2][kTile];  // 2^-exponent
@@ -127,23 +135,29 @@ template <bool E4> struct Ctl {
     uint64_t s_full[2];           // scores are in TMEM
     uint64_t p_full[2];           // weights are in TMEM (one arrival per warp)
     uint64_t o_full[2];           // the product with V is complete
-    uint64_t q_full;              // Q is in shared memory
+    uint64_t q_full;              // the softmax warps have written Q (bf16, or its codes)
+    uint64_t qt_full[2];          // Q has landed by TMA in buffer 0, 1
+    uint64_t q_empty[2];          // no product will read the buffer any more
     uint64_t poison_full;         // poison holds this segment's new tokens
     uint64_t done;
     uint32_t poison_slot[kMaxStages][4];
     uint32_t poison[4];           // new tokens with non-finite values
     unsigned qmax[2];
     int warp_sum[kThreads / 32];
-    int last_fill[kMaxStages];
+    int last_fill[kMaxStages], last_q[2];
     uint32_t tmem;
     int abort;
     int start_b, start_ub;
+    float2 xch[2][kTile];         // (mu, l) of the slots' rows
     Tables<E4> tab;
 };
 
+static_assert(alignof(Ctl<true>) == 16 && offsetof(Ctl<true>, tab) % 16 == 0 && sizeof(float[kTile]) % 16 == 0,
+              "16-byte reads of the tables");
+
 template <int D, bool E4> constexpr size_t smem_bytes()
 {
-    return 1024 + 2 * (size_t)Cfg<D, E4>::kQTile + (size_t)Cfg<D, E4>::kStages * kSlotBytes + sizeof(Ctl<E4>);
+    return 2 * (size_t)Cfg<D, E4>::kQTile + (size_t)Cfg<D, E4>::kStages * kSlotBytes + sizeof(Ctl<E4>);
 }
 static_assert(smem_bytes<128, false>() <= 232448 && smem_bytes<128, true>() <= 232448 &&
                   smem_bytes<64, false>() <= 232448 && smem_bytes<64, true>() <= 232448,
@@ -189,7 +203,7 @@ __device__ __forceinline__ int tiles_of(const AttnParams &p, int n)
 }
 
 struct Seg {
-    bool prefix, bad;
+    bool prefix, bad, tq;
     int b, h;
     int row0, nrows;  // first row among the head's B*T*G, rows
     int t0, n, nt;    // tiles t0 .. t0 + n - 1 of nt are this CTA's
@@ -197,10 +211,10 @@ struct Seg {
     int hn;           // 1: tile 0 is the new tokens'
     int rb;           // row block within the source
     int id;           // number among its kind
-    bool first;       // the CTA's first segment
+    bool first;       // the CTA's stretch starts in it
 
     __device__ bool none() const { return keys == 0 && !hn; }  // a unit without a tile
-    __device__ bool whole() const { return t0 == 0 && n == nt; }
+    __device__ bool whole() const { return n == nt; }
     __device__ bool draft() const { return hn && t0 == 0; }    // this piece holds the new tokens' tile
     __device__ bool pair() const { return nrows > kTile; }
     __device__ int slot_rows(int s) const { return pair() ? min(kTile, nrows - kTile * s) : nrows; }
@@ -208,68 +222,76 @@ struct Seg {
     __device__ int valid(int tile) const { return min(kTile, keys - key0(tile)); }
 };
 
-// Walks the segments of a CTA's stretch; every role walks the same ones.
+// Walks the segments of a CTA's stretch; every role walks the same ones.  A
+// segment takes kSegCost units ahead of its tiles' units; a stretch that holds
+// only such units of it has no part in it.
 struct Walk {
-    int u, u1, b, ub, raw, raw_next;
-    bool first;
+    int u, u0, u1, b, ub, raw, raw_next;
 
-    __device__ void start(const AttnParams &p, int u0, int u1_, int b0, int ub0)
+    __device__ void start(const AttnParams &p, int u0_, int u1_, int b0, int ub0)
     {
-        u = u0;
+        u = u0 = u0_;
         u1 = u1_;
         b = b0;
         ub = ub0;
-        first = true;
         raw = raw_len(p, b);
         raw_next = raw_len(p, b + 1);
     }
 
+    // Tiles of [u, u1) in the segment of units us .. us + kSegCost + nt - 1; moves u to its end.
+    __device__ void cut(Seg &s, int us)
+    {
+        const int e = min(u1, us + kSegCost + s.nt);
+        s.first = u0 >= us;
+        s.t0 = max(u - us - kSegCost, 0);
+        s.n = max(e - us - kSegCost, 0) - s.t0;
+        u = e;
+    }
+
     __device__ bool next(const AttnParams &p, Seg &s)
     {
-        if (u >= u1)
-            return false;
-        s.first = first;
-        first = false;
-        if (u < p.UP) {
-            s.id = u / p.ntp;
-            s.t0 = u - s.id * p.ntp;
-            s.nt = p.ntp;
-            s.n = min(s.nt - s.t0, u1 - u);
-            s.prefix = true;
-            s.bad = false;
-            s.b = 0;
-            s.h = s.id / p.nbp;
-            s.rb = s.id - s.h * p.nbp;
-            s.row0 = s.rb * 2 * kTile;
-            s.nrows = min(2 * kTile, p.B * p.T * p.G - s.row0);
-            s.keys = p.Lp;
-            s.hn = 0;
-            u += s.n;
-            return true;
+        while (u < u1) {
+            if (u < p.UP) {
+                const int per = p.ntp + kSegCost;
+                s.id = u / per;
+                s.nt = p.ntp;
+                s.prefix = true;
+                s.bad = s.tq = false;
+                s.b = 0;
+                s.h = s.id / p.nbp;
+                s.rb = s.id - s.h * p.nbp;
+                s.row0 = s.rb * 2 * kTile;
+                s.nrows = min(2 * kTile, p.B * p.T * p.G - s.row0);
+                s.keys = p.Lp;
+                s.hn = 0;
+                cut(s, s.id * per);
+            } else {
+                const Len len = clean_len(p, raw);
+                s.nt = tiles_of(p, len.n);
+                const int per = s.nt + kSegCost, rel = (u - ub) / per;
+                s.prefix = false;
+                s.tq = p.tma_q;
+                s.bad = len.bad;
+                s.b = b;
+                s.h = rel / p.nbs;
+                s.rb = rel - s.h * p.nbs;
+                s.row0 = b * p.T * p.G + s.rb * 2 * kTile;
+                s.nrows = min(2 * kTile, p.T * p.G - s.rb * 2 * kTile);
+                s.keys = len.n;
+                s.hn = p.has_new;
+                s.id = (b * p.H + s.h) * p.nbs + s.rb;
+                cut(s, ub + rel * per);
+                if (u == ub + p.H * p.nbs * per) {
+                    ub = u;
+                    ++b;
+                    raw = raw_next;
+                    raw_next = raw_len(p, b + 1);
+                }
+            }
+            if (s.n > 0)
+                return true;
         }
-        const Len len = clean_len(p, raw);
-        const int nt = tiles_of(p, len.n), local = u - ub, rel = local / nt;
-        s.prefix = false;
-        s.bad = len.bad;
-        s.b = b;
-        s.h = rel / p.nbs;
-        s.rb = rel - s.h * p.nbs;
-        s.t0 = local - rel * nt;
-        s.nt = nt;
-        s.n = min(nt - s.t0, u1 - u);
-        s.row0 = b * p.T * p.G + s.rb * 2 * kTile;
-        s.nrows = min(2 * kTile, p.T * p.G - s.rb * 2 * kTile);
-        s.keys = len.n;
-        s.hn = p.has_new;
-        s.id = (b * p.H + s.h) * p.nbs + s.rb;
-        u += s.n;
-        if (u == ub + p.H * p.nbs * nt) {
-            ub = u;
-            ++b;
-            raw = raw_next;
-            raw_next = raw_len(p, b + 1);
-        }
-        return true;
+        return false;
     }
 };
 
@@ -289,11 +311,28 @@ template <int D, bool E4> struct Fills {
 // ---- waits -------------------------------------------------------------------------
 
 // Waits for phase n (counted from 0) of the barrier; after a wait that gave up
-// every later one returns soon, so that each role still ends.
+// every later one returns at once, so that each role still ends.  The timer is
+// read only after many tries: reading it costs more than a usual wait.
 template <class C> __device__ __forceinline__ void await(C &ctl, uint64_t *bar, uint32_t n)
 {
-    if (*(volatile int *)&ctl.abort || !mbar_wait_bounded(bar, n & 1u, &ctl.abort, kWaitNs))
-        *(volatile int *)&ctl.abort = 1;
+    if (mbar_try_wait_hint(bar, n & 1u, kHintNs))
+        return;
+    uint64_t t0 = 0;
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait_hint(bar, n & 1u, kHintNs))
+            return;
+        if ((it & 15u) == 0) {
+            if (*(volatile int *)&ctl.abort)
+                return;
+            const uint64_t t = globaltimer_ns();
+            if (t0 == 0) {
+                t0 = t;
+            } else if (t - t0 > kWaitNs) {
+                *(volatile int *)&ctl.abort = 1;
+                return;
+            }
+        }
+    }
 }
 
 __device__ __forceinline__ void bar_sync(int id, int threads)
@@ -310,6 +349,15 @@ __device__ __forceinline__ unsigned pack_bf16(float lo, float hi)
 {
     const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const unsigned *>(&r);
+}
+
+// (x0, x1) = (x0, x1) * (a0, a1) + (b0, b1) on float bits
+__device__ __forceinline__ void fma_pair(uint32_t &x0, uint32_t &x1, float a0, float a1, float b0, float b1)
+{
+    float r0, r1;
+    unpack2(fma2(pack2(__uint_as_float(x0), __uint_as_float(x1)), pack2(a0, a1), pack2(b0, b1)), r0, r1);
+    x0 = __float_as_uint(r0);
+    x1 = __float_as_uint(r1);
 }
 
 // Scale exponent of a magnitude's bf16 bits: smallest e with m <= 448 * 2^e.
@@ -330,12 +378,16 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
 {
     using C = Cfg<D, E4>;
     constexpr int kStages = C::kStages;
-    extern __shared__ unsigned char smem_raw[];
-    unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) unsigned char smem[];
     unsigned char *ring = smem + 2 * C::kQTile;
     Ctl<E4> &ctl = *reinterpret_cast<Ctl<E4> *>(ring + kStages * kSlotBytes);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+    if (smem_u32(smem) & 1023u) {  // the swizzled tiles want 1024-byte alignment; without static shared memory they have it
+        if (tid == 0 && p.status)
+            atomicOr(p.status, SV_ATTN_TIMEOUT);
+        return;
+    }
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&ctl.full[s], 1);
@@ -347,11 +399,15 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
             mbar_init(&ctl.s_full[s], 1);
             mbar_init(&ctl.p_full[s], 4);
             mbar_init(&ctl.o_full[s], 1);
+            mbar_init(&ctl.qt_full[s], 1);
+            mbar_init(&ctl.q_empty[s], 1);
         }
         mbar_init(&ctl.q_full, kSoftmaxThreads);
         mbar_init(&ctl.poison_full, 1);
         mbar_init(&ctl.done, 1);
+        ctl.last_q[0] = ctl.last_q[1] = -1;
         ctl.abort = 0;
+        ctl.qmax[0] = ctl.qmax[1] = 0;
         ctl.start_b = 0;
         ctl.start_ub = p.UP;
         fence_mbar_init();
@@ -368,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
     const int bs = min(p.B, tid * chunk), be = min(p.B, bs + chunk);
     int mine = 0;
     for (int b = bs; b < be; ++b)
-        mine += tiles_of(p, clean_len(p, raw_len(p, b)).n);
+        mine += (kSegCost + tiles_of(p, clean_len(p, raw_len(p, b)).n));
     int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -398,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
         const bool holds = target >= ub && target < ub + per * mine;
         if (holds || blockIdx.x == 0)
             for (int b = bs; b < be; ++b) {
-                const int next = ub + per * tiles_of(p, clean_len(p, raw_len(p, b)).n);
+                const int next = ub + per * (kSegCost + tiles_of(p, clean_len(p, raw_len(p, b)).n));
                 if (target >= ub && target < next) {
                     ctl.start_b = b;
                     ctl.start_ub = ub;
@@ -416,6 +472,8 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
     walk.start(p, u0, u1, ctl.start_b, ctl.start_ub);
     Seg seg;
 
+    if (warp >= 8) {
+    regs_dec<kRegsOther>();
     if (warp == 8) {
         // ---- producer ----
         if (lane == 0) {
@@ -426,10 +484,26 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
                     await(ctl, &ctl.empty[s], fill / kStages - 1);
                 return !*(volatile int *)&ctl.abort;
             };
-            bool ok = true;
+            bool ok = true, by_threads = false;
+            uint32_t ntq = 0;
             while (ok && walk.next(p, seg)) {
                 if (seg.none())
                     continue;
+                if (seg.tq) {
+                    // buffer j & 1 was read last by TMA segment j - 2, or by the segments whose Q came otherwise
+                    const uint32_t qb = ntq & 1u, use = (ntq >> 1) + (by_threads ? 1 : 0);
+                    if (use > 0)
+                        await(ctl, &ctl.q_empty[qb], use - 1);
+                    if (*(volatile int *)&ctl.abort)
+                        break;
+                    mbar_arrive_expect_tx(&ctl.qt_full[qb], (uint32_t)seg.nrows * D * 2);
+                    for (int x = 0; x < D; x += 64)
+                        tma_load_4d(smem + qb * C::kQTile + (x / 64) * kPanel, &maps.q, x, seg.h * p.G, 0, seg.b, &ctl.qt_full[qb]);
+                    ctl.last_q[qb] = (int)(ntq >> 1);
+                    ++ntq;
+                } else {
+                    by_threads = true;
+                }
                 for (int i = 0; i < seg.n && ok; ++i) {
                     const int tile = seg.t0 + i;
                     const bool draft = seg.hn && tile == 0;
@@ -472,13 +546,24 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
             constexpr int kSw8 = D;             // an e4m3 row is D bytes: its swizzle
             constexpr uint32_t kAtom8 = 8 * D;  // 8 rows of it
             uint32_t base = 0;                  // ring fills before this segment
-            uint32_t nq = 0, npv[2] = {0, 0};
+            uint32_t nq = 0, npv[2] = {0, 0}, ntq = 0;
+            bool by_threads = false;
             while (walk.next(p, seg)) {
                 if (seg.none())
                     continue;
                 const bool pair = seg.pair(), draft = seg.draft();
                 const int njobs = pair ? 2 * seg.n : seg.n;
-                await(ctl, &ctl.q_full, nq++);
+                const uint32_t qb = seg.tq ? ntq & 1u : 0u;
+                if (seg.tq && ntq == 0 && by_threads) {
+                    tc_commit(&ctl.q_empty[0]);  // the earlier segments' products with Q
+                    tc_commit(&ctl.q_empty[1]);
+                }
+                if (seg.tq && (!E4 || draft))
+                    await(ctl, &ctl.qt_full[qb], ntq >> 1);
+                else
+                    await(ctl, &ctl.q_full, nq++);
+                ntq += seg.tq;
+                by_threads |= !seg.tq;
                 tc_fence_after();
                 bool q8 = E4 && !draft;
                 auto scores = [&](int q) {
@@ -493,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
                     const int st = (int)(f % kStages);
                     await(ctl, &ctl.full[st], f / kStages);
                     tc_fence_after();
-                    const unsigned char *qt = smem + (pair ? s : 0) * C::kQTile, *kt = ring + st * kSlotBytes;
+                    const unsigned char *qt = smem + (pair ? s : qb) * C::kQTile, *kt = ring + st * kSlotBytes;
                     const uint32_t d = tmem + 256 + 128 * s;
                     if (!E4 || dr) {
 #pragma unroll
@@ -504,13 +589,16 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
                         const uint64_t dk = smem_desc(kt, 16, kAtom8, kSw8);
 #pragma unroll
                         for (int part = 0; part < 2; ++part) {
-                            const uint64_t dq = smem_desc(qt + part * (C::kQTile / 2), 16, kAtom8, kSw8);
+                            // the second term: the next panel (D = 128), or the other half of the same rows
+                            const uint64_t dq = smem_desc_k128(qt + (D == 128 ? part * kPanel : 0)) + (D == 64 ? 4u * part : 0u);
 #pragma unroll
                             for (int kk = 0; kk < D / 32; ++kk)
                                 tc_mma_f8(d, dq + 2u * kk, dk + 2u * kk, idS8, part || kk);
                         }
                     }
                     tc_commit(&ctl.s_full[s]);
+                    if (seg.tq && q == njobs - 1)
+                        tc_commit(&ctl.q_empty[qb]);
                     if (Fills<D, E4>::two(dr) && (!pair || s == 1))
                         tc_commit(&ctl.empty[st]);  // no later job reads these keys
                 };
@@ -627,7 +715,9 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
                 }
             }
         }
+    }
     } else {
+        regs_inc<kRegsSoftmax>();
         // ---- softmax and epilogue: slot s, row r ----
         const int s = warp >> 2, wq = warp & 3, r = wq * 32 + lane;
         const int pt = tid & 127;  // place in the slot's 128 threads
@@ -635,6 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
         const uint32_t tS = tmem + lanes + 256 + 128 * s, tO = tmem + lanes + 128 * s;
         uint32_t nj = 0, npois = 0;  // jobs of the slot, segments with new tokens so far
         uint32_t ntab = 0;           // e4m3 tiles of the slot so far
+        uint32_t ntq = 0;            // segments whose Q came by TMA
         while (walk.next(p, seg)) {
             const bool pair = seg.pair(), draft = seg.draft(), none = seg.none();
             const int njobs = none ? 0 : pair ? 2 * seg.n : seg.n;
@@ -644,75 +735,70 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
             bool poison = seg.bad;
             float mu = -INFINITY, l = 0.0f;
             float cq = p.c;  // factor of an e4m3 job's scores
-            unsigned char *qt = smem + (pair ? s : 0) * C::kQTile;
-            // this thread's 16-byte pieces of Q: rows of its slot's tile, or half of the shared tile's
-            constexpr int kPc = D / 8;                              // pieces of a row
-            const int q_first = pair ? 0 : kTile / 2 * s, q_rows = pair ? kTile : kTile / 2;
+            const uint32_t qb = seg.tq ? ntq & 1u : 0u;
+            unsigned char *qt = smem + (pair ? s : qb) * C::kQTile;
+            // the 16-byte pieces of Q's rows, dealt to the slot's threads, or to both slots' when they share the tile
+            constexpr int kPc = D / 8;  // pieces of a row
+            const int q_from = pair ? pt : tid, q_step = pair ? 128 : 256;
+            const int q_end = cdiv(rows * kPc, 32) * 32;  // whole warps
             auto q_piece = [&](int row, int x) {
                 return reinterpret_cast<uint4 *>(qt + (x / 8) * kPanel + row * 128 + (((x & 7) ^ (row & 7)) * 16));
             };
-            // Q in bf16 -> two e4m3 terms in place; every thread of both slots takes part
+            // Q in bf16 -> two e4m3 terms, in the place of the same row; every thread of both slots takes part
             auto to_codes = [&]() {
-                bar_sync(1, kSoftmaxThreads);  // no product reads Q in bf16 any more, qmax is cleared
-                uint4 x[16];
-                unsigned m = 0;
+                bar_sync(1, kSoftmaxThreads);  // no product reads Q in bf16 any more
+                unsigned qm = 0;
+                for (int e = q_from; e < q_end; e += q_step) {
+                    if (e >= rows * kPc)  // behind the rows: whatever the buffer held
+                        continue;
+                    const uint4 v = *q_piece(e / kPc, e % kPc);
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    const int e = pt + 128 * k, row = q_first + e / kPc;
-                    if (e < q_rows * kPc) {
-                        x[k] = *q_piece(row, e % kPc);
-                        const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const uint32_t lo = w[j] & 0x7fffu, hi = (w[j] >> 16) & 0x7fffu;
-                            m = max(m, max(lo >= 0x7f80u ? 0u : lo, hi >= 0x7f80u ? 0u : hi));
-                        }
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t lo = w[j] & 0x7fffu, hi = (w[j] >> 16) & 0x7fffu;
+                        qm = max(qm, max(lo >= 0x7f80u ? 0u : lo, hi >= 0x7f80u ? 0u : hi));
                     }
                 }
-                m = __reduce_max_sync(0xffffffffu, m);
+                qm = __reduce_max_sync(0xffffffffu, qm);
                 if (lane == 0)
-                    atomicMax(&ctl.qmax[pair ? s : 0], m);
+                    atomicMax(&ctl.qmax[pair ? s : 0], qm);
                 bar_sync(1, kSoftmaxThreads);
                 const int e2 = code_exponent(ctl.qmax[pair ? s : 0]);
                 const float f = pow2i(-e2);
                 cq = p.c * pow2i(e2);
+#pragma unroll 1
+                for (int e = q_from; e < q_end; e += q_step) {  // a warp holds whole rows
+                    const int row = e / kPc, x0 = e % kPc;
+                    const uint4 x = *q_piece(row, x0);
+                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                    uint32_t hi[2], lo[2];
 #pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    const int e = pt + 128 * k, row = q_first + e / kPc, x0 = e % kPc;
-                    if (e < q_rows * kPc) {
-                        const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-                        uint32_t hi[2], lo[2];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            float a = __uint_as_float(w[j] << 16), b = __uint_as_float(w[j] & 0xffff0000u);
-                            a = (w[j] & 0x7f80u) == 0x7f80u ? nan_f() : a * f;
-                            b = (w[j] & 0x7f800000u) == 0x7f800000u ? nan_f() : b * f;
-                            const uint32_t ch = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-                            const float2 back = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)ch, __NV_E4M3)));
-                            const uint32_t cl = __nv_cvt_float2_to_fp8x2(make_float2(a - back.x, b - back.y), __NV_SATFINITE, __NV_E4M3);
-                            hi[j >> 1] = (j & 1) ? hi[j >> 1] | (ch << 16) : ch;
-                            lo[j >> 1] = (j & 1) ? lo[j >> 1] | (cl << 16) : cl;
-                        }
-                        // 8 codes at byte 8 * x0 of a D-byte row, 16-byte chunks swizzled as TMA does for rows of D bytes
-                        const int ch16 = x0 >> 1;
-                        const int sw = D == 128 ? ch16 ^ (row & 7) : ch16 ^ ((row >> 1) & 3);
-                        unsigned char *at = qt + row * D + sw * 16 + (x0 & 1) * 8;
-                        *reinterpret_cast<uint2 *>(at) = make_uint2(hi[0], hi[1]);
-                        *reinterpret_cast<uint2 *>(at + C::kQTile / 2) = make_uint2(lo[0], lo[1]);
+                    for (int j = 0; j < 4; ++j) {
+                        float a = __uint_as_float(w[j] << 16), b = __uint_as_float(w[j] & 0xffff0000u);
+                        a = (w[j] & 0x7f80u) == 0x7f80u ? nan_f() : a * f;
+                        b = (w[j] & 0x7f800000u) == 0x7f800000u ? nan_f() : b * f;
+                        const uint32_t ch = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+                        const float2 back = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)ch, __NV_E4M3)));
+                        const uint32_t cl = __nv_cvt_float2_to_fp8x2(make_float2(a - back.x, b - back.y), __NV_SATFINITE, __NV_E4M3);
+                        hi[j >> 1] = (j & 1) ? hi[j >> 1] | (ch << 16) : ch;
+                        lo[j >> 1] = (j & 1) ? lo[j >> 1] | (cl << 16) : cl;
                     }
+                    __syncwarp();
+                    // 8 codes at byte 8 * x0 of a 128-byte row (D = 64: the second terms at byte 64 of it)
+                    auto at = [&](int byte) { return qt + row * 128 + ((((byte >> 4) ^ (row & 7)) << 4) | (byte & 8)); };
+                    *reinterpret_cast<uint2 *>(at(8 * x0)) = make_uint2(hi[0], hi[1]);
+                    *reinterpret_cast<uint2 *>(D == 128 ? at(8 * x0) + kPanel : at(8 * x0 + 64)) = make_uint2(lo[0], lo[1]);
                 }
                 fence_async_shared();
                 mbar_arrive(&ctl.q_full);
             };
-            uint32_t seen[4] = {0, 0, 0, 0};  // new tokens that this row sees
+            uint32_t seen[4] = {0, 0, 0, 0};  // new tokens that this row sees; only ever indexed by constants
             bool convert = false;             // Q has yet to go from bf16 to codes
             if (!none) {
-                if (E4 && pt == 0)
-                    ctl.qmax[s] = 0;
+                if (!seg.tq) {
 #pragma unroll 4
-                for (int k = 0; k < 16; ++k) {
-                    const int e = pt + 128 * k, row = q_first + e / kPc, x = e % kPc;
-                    if (e < q_rows * kPc) {
+                    for (int e = q_from; e < q_end; e += q_step) {
+                        const int row = e / kPc, x = e % kPc;
                         uint4 v = make_uint4(0, 0, 0, 0);
                         if (row < rows) {
                             const int R = row0 + row, tok = R / p.G, b = tok / p.T;
@@ -722,9 +808,14 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
                         *q_piece(row, x) = v;
                     }
                 }
+                if (seg.tq && E4)
+                    await(ctl, &ctl.qt_full[qb], ntq >> 1);
+                ntq += seg.tq;
                 if (!E4 || draft) {
-                    fence_async_shared();
-                    mbar_arrive(&ctl.q_full);
+                    if (!seg.tq) {
+                        fence_async_shared();
+                        mbar_arrive(&ctl.q_full);
+                    }
                     convert = E4 && seg.n > 1;
                 } else {
                     to_codes();
@@ -781,20 +872,15 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
                 const int i = pair ? q >> 1 : q, tile = seg.t0 + i;
                 const bool dr = draft && i == 0;
                 const int valid = dr ? kTile : seg.valid(tile);
-                const float *kk = nullptr, *ev = nullptr, *inv = nullptr;
+                const int tb = (int)(ntab & 1u);
                 if constexpr (E4) {
-                    if (!dr) {
-                        const int tb = (int)(ntab & 1u);
-                        ctl.tab.kk[s][tb][pt] = cq * __uint_as_float(sk << 23);
-                        ctl.tab.ev[s][tb][pt] = (float)((int)sv_ - 127);
-                        ctl.tab.inv[s][tb][pt] = __uint_as_float((254u - min(sv_, 254u)) << 23);
+                    ++ntab;
+                    ctl.tab.kk[s][tb][pt] = dr ? p.c : cq * __uint_as_float(sk << 23);
+                    ctl.tab.ev[s][tb][pt] = dr ? 0.0f : (float)((int)sv_ - 127);
+                    ctl.tab.inv[s][tb][pt] = dr ? 1.0f : __uint_as_float((254u - min(sv_, 254u)) << 23);
+                    if (!dr)
                         fetch_scales(tile + step);
-                        ++ntab;
-                        bar_sync(2 + s, 128);
-                        kk = ctl.tab.kk[s][tb];
-                        ev = ctl.tab.ev[s][tb];
-                        inv = ctl.tab.inv[s][tb];
-                    }
+                    bar_sync(2 + s, 128);
                 }
                 await(ctl, &ctl.s_full[s], nj);
                 tc_fence_after();
@@ -803,38 +889,46 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
                     convert = false;
                 }
                 if (active) {
-                    // the row's maximum of y over the tile
+                    const bool masked = dr || valid < kTile;
+                    // the row's maximum over the tile; what is masked, or scaled by key, goes back in its place.
+                    // The loops stay rolled: a tile's code is then a few KB, and no warp waits for instructions.
                     float mx = -INFINITY;
-#pragma unroll
+#pragma unroll 1
                     for (int c0 = 0; c0 < kTile; c0 += 32) {
                         uint32_t x[32];
                         tmem_ld32_nowait(tS + c0, x);
                         tmem_wait_ld();
+                        if constexpr (E4) {  // y = score * the key's factor + the exponent of the value's scale
+                            const float4 *kk4 = reinterpret_cast<const float4 *>(&ctl.tab.kk[s][tb][c0]);
+                            const float4 *ev4 = reinterpret_cast<const float4 *>(&ctl.tab.ev[s][tb][c0]);
+#pragma unroll
+                            for (int k = 0; k < 32; k += 4) {
+                                const float4 a = kk4[k / 4], e = ev4[k / 4];
+                                fma_pair(x[k], x[k + 1], a.x, a.y, e.x, e.y);
+                                fma_pair(x[k + 2], x[k + 3], a.z, a.w, e.z, e.w);
+                            }
+                        }
+                        if (masked) {
+                            const int left = valid - c0;
+                            const uint32_t sw = c0 == 0 ? seen[0] : c0 == 32 ? seen[1] : c0 == 64 ? seen[2] : seen[3];
+                            const uint32_t ok = dr ? sw : left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1u;
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                x[k] = (ok >> k) & 1u ? x[k] : 0xff800000u;
+                        }
+                        if (E4 || masked)
+                            tmem_st32(tS + c0, x);
                         float m0 = -INFINITY, m1 = -INFINITY;
-                        if (valid - c0 < 32 || dr) {
-                            const uint32_t ok = dr ? seen[c0 >> 5] : valid <= c0 ? 0u : valid - c0 >= 32 ? 0xffffffffu : (1u << (valid - c0)) - 1u;
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) {
-                                float y = __uint_as_float(x[k]);
-                                if (E4 && !dr)
-                                    y = fmaf(y, kk[c0 + k], ev[c0 + k]);
-                                m0 = fmaxf(m0, (ok >> k) & 1u ? y : -INFINITY);
-                            }
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < 32; k += 2) {
-                                float y0 = __uint_as_float(x[k]), y1 = __uint_as_float(x[k + 1]);
-                                if (E4 && !dr) {
-                                    y0 = fmaf(y0, kk[c0 + k], ev[c0 + k]);
-                                    y1 = fmaf(y1, kk[c0 + k + 1], ev[c0 + k + 1]);
-                                }
-                                m0 = fmaxf(m0, y0);
-                                m1 = fmaxf(m1, y1);
-                            }
+                        for (int k = 0; k < 32; k += 4) {
+                            m0 = fmaxf(m0, fmaxf(__uint_as_float(x[k]), __uint_as_float(x[k + 1])));
+                            m1 = fmaxf(m1, fmaxf(__uint_as_float(x[k + 2]), __uint_as_float(x[k + 3])));
                         }
                         mx = fmaxf(mx, fmaxf(m0, m1));
                     }
-                    if (!E4 || dr)
+                    if (E4 || masked)
+                        tmem_wait_st();
+                    if (!E4)
                         mx *= p.c;
                     const bool grow = mx > mu + C::kSlack || (mu == -INFINITY && mx > mu);
                     if (__any_sync(0xffffffffu, grow)) {
@@ -845,73 +939,82 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
                         if (q >= 2) {  // O holds earlier tiles: their product must be complete
                             await(ctl, &ctl.o_full[s], nj - 1);
                             tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                             for (int c0 = 0; c0 < D; c0 += 32) {
-                                uint32_t x[32];
-                                tmem_ld32_nowait(tO + c0, x);
+                                uint32_t o[32];
+                                tmem_ld32_nowait(tO + c0, o);
                                 tmem_wait_ld();
 #pragma unroll
                                 for (int k = 0; k < 32; ++k)
-                                    x[k] = f == 0.0f ? 0u : __float_as_uint(__uint_as_float(x[k]) * f);
-                                tmem_st32(tO + c0, x);
+                                    o[k] = f == 0.0f ? 0u : __float_as_uint(__uint_as_float(o[k]) * f);
+                                tmem_st32(tO + c0, o);
                             }
                         }
                     }
-                    const float R = mu == -INFINITY ? 0.0f : mu - C::kBase;
-                    float l0 = 0.0f, l1 = 0.0f;
-#pragma unroll
-                    for (int c0 = 0; c0 < kTile; c0 += 32) {
-                        uint32_t x[32];
-                        tmem_ld32_nowait(tS + c0, x);
-                        tmem_wait_ld();
-                        if (valid - c0 < 32 || dr) {
-                            const uint32_t ok = dr ? seen[c0 >> 5] : valid <= c0 ? 0u : valid - c0 >= 32 ? 0xffffffffu : (1u << (valid - c0)) - 1u;
-#pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                x[k] = (ok >> k) & 1u ? x[k] : 0xff800000u;
-                        }
-                        if (!E4 || dr) {
-#pragma unroll
-                            for (int k = 0; k < 32; k += 2) {
-                                const float w0 = ex2(fmaf(__uint_as_float(x[k]), p.c, -R));
-                                const float w1 = ex2(fmaf(__uint_as_float(x[k + 1]), p.c, -R));
-                                l0 += w0;
-                                l1 += w1;
-                                x[k >> 1] = pack_bf16(w0, w1);
-                            }
-                            tmem_st16(tS + (c0 >> 1), x);
-                        } else {
-                            uint32_t w24[24];
+                    const float nR = mu == -INFINITY ? 0.0f : C::kBase - mu;
+                    const unsigned long long nR2 = pack2(nR, nR), c2 = pack2(p.c, p.c);
+                    unsigned long long la = 0, lb = 0;  // four partial sums
+                    if (!E4 || dr) {
+#pragma unroll 1
+                        for (int c0 = 0; c0 < kTile; c0 += 32) {
+                            uint32_t x[32];
+                            tmem_ld32_nowait(tS + c0, x);
+                            tmem_wait_ld();
 #pragma unroll
                             for (int k = 0; k < 32; k += 4) {
                                 float w[4];
+                                const unsigned long long a = pack2(__uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+                                const unsigned long long b = pack2(__uint_as_float(x[k + 2]), __uint_as_float(x[k + 3]));
+                                unpack2(E4 ? add2(a, nR2) : fma2(a, c2, nR2), w[0], w[1]);
+                                unpack2(E4 ? add2(b, nR2) : fma2(b, c2, nR2), w[2], w[3]);
 #pragma unroll
-                                for (int j = 0; j < 4; ++j) {
-                                    w[j] = ex2(fmaf(__uint_as_float(x[k + j]), kk[c0 + k + j], ev[c0 + k + j]) - R);
-                                    if (j & 1)
-                                        l1 = fmaf(w[j], inv[c0 + k + j], l1);
-                                    else
-                                        l0 = fmaf(w[j], inv[c0 + k + j], l0);
-                                }
+                                for (int j = 0; j < 4; ++j)
+                                    w[j] = ex2(w[j]);
+                                la = add2(la, pack2(w[0], w[1]));
+                                lb = add2(lb, pack2(w[2], w[3]));
+                                x[k >> 1] = pack_bf16(w[0], w[1]);
+                                x[(k >> 1) + 1] = pack_bf16(w[2], w[3]);
+                            }
+                            tmem_st16(tS + (c0 >> 1), x);
+                        }
+                    } else if constexpr (E4) {
+#pragma unroll 1
+                        for (int c0 = 0; c0 < kTile; c0 += 32) {
+                            const float4 *inv4 = reinterpret_cast<const float4 *>(&ctl.tab.inv[s][tb][c0]);
+                            uint32_t x[32], t8[24];
+                            tmem_ld32_nowait(tS + c0, x);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int k = 0; k < 32; k += 4) {
+                                float w[4];
+                                unpack2(add2(pack2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), nR2), w[0], w[1]);
+                                unpack2(add2(pack2(__uint_as_float(x[k + 2]), __uint_as_float(x[k + 3])), nR2), w[2], w[3]);
+#pragma unroll
+                                for (int j = 0; j < 4; ++j)
+                                    w[j] = ex2(w[j]);
+                                const float4 v = inv4[k / 4];
+                                la = fma2(pack2(w[0], w[1]), pack2(v.x, v.y), la);
+                                lb = fma2(pack2(w[2], w[3]), pack2(v.z, v.w), lb);
                                 // three e5m2 terms of f16 weights: the upper bytes of w, of w - first, of the rest
-                                __half2 a = __floats2half2_rn(w[0], w[1]), b = __floats2half2_rn(w[2], w[3]);
+                                __half2 ha = __floats2half2_rn(w[0], w[1]), hb = __floats2half2_rn(w[2], w[3]);
 #pragma unroll
                                 for (int part = 0; part < 2; ++part) {
-                                    const uint32_t ua = *reinterpret_cast<uint32_t *>(&a), ub = *reinterpret_cast<uint32_t *>(&b);
-                                    w24[part * 8 + (k >> 2)] = __byte_perm(ua, ub, 0x7531);
-                                    const uint32_t ta = ua & 0xff00ff00u, tb = ub & 0xff00ff00u;
-                                    a = __hsub2(a, *reinterpret_cast<const __half2 *>(&ta));
-                                    b = __hsub2(b, *reinterpret_cast<const __half2 *>(&tb));
+                                    const uint32_t ua = *reinterpret_cast<uint32_t *>(&ha), ub = *reinterpret_cast<uint32_t *>(&hb);
+                                    t8[8 * part + (k >> 2)] = __byte_perm(ua, ub, 0x7531);
+                                    const uint32_t ta = ua & 0xff00ff00u, tb2 = ub & 0xff00ff00u;
+                                    ha = __hsub2(ha, *reinterpret_cast<const __half2 *>(&ta));
+                                    hb = __hsub2(hb, *reinterpret_cast<const __half2 *>(&tb2));
                                 }
-                                const uint32_t la = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(a), __NV_SATFINITE, __NV_E5M2);
-                                const uint32_t lb = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(b), __NV_SATFINITE, __NV_E5M2);
-                                w24[16 + (k >> 2)] = la | (lb << 16);
+                                const uint32_t ca = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(ha), __NV_SATFINITE, __NV_E5M2);
+                                const uint32_t cb = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(hb), __NV_SATFINITE, __NV_E5M2);
+                                t8[16 + (k >> 2)] = ca | (cb << 16);
                             }
-                            const uint32_t at = tS + (c0 >> 5) * 24;
-                            tmem_st16(at, w24);
-                            tmem_st8(at + 16, w24 + 16);
+                            tmem_st16(tS + (c0 >> 5) * 24, t8);
+                            tmem_st8(tS + (c0 >> 5) * 24 + 16, t8 + 16);
                         }
                     }
+                    float l0, l1;
+                    unpack2(add2(la, lb), l0, l1);
                     l += l0 + l1;
                     tmem_wait_st();
                 }
@@ -937,11 +1040,10 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
                 l = nan_f();
             float f_own = mu == -INFINITY ? 0.0f : 1.0f, f_oth = 0.0f;
             if (!pair) {
-                bar_sync(1, kSoftmaxThreads);  // all of both slots' products are complete, Q is free
-                float2 *xch = reinterpret_cast<float2 *>(smem);
-                xch[s * kTile + r] = make_float2(mu, l);
-                bar_sync(1, kSoftmaxThreads);
-                const float2 o = xch[(1 - s) * kTile + r];
+                ctl.xch[s][r] = make_float2(mu, l);
+                bar_sync(1, kSoftmaxThreads);  // both slots' products are complete
+                tc_fence_after();
+                const float2 o = ctl.xch[1 - s][r];
                 const float mn = fmaxf(mu, o.x);
                 f_own = mu == -INFINITY ? 0.0f : ex2(mu - mn);
                 f_oth = o.x == -INFINITY ? 0.0f : ex2(o.x - mn);
@@ -1017,7 +1119,9 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
                     p.lse[orow] = l == 0.0f ? -INFINITY : (R + log2f(l)) * 0.69314718055994531f;
             }
             tc_fence_before();
-            bar_sync(1, kSoftmaxThreads);  // O has been read by both slots, Q and the exchange may be overwritten
+            if (E4 && pt == 0)
+                ctl.qmax[s] = 0;  // read last before this segment's products
+            bar_sync(1, kSoftmaxThreads);  // O has been read by both slots, the exchange may be overwritten
             tc_fence_after();
         }
     }
@@ -1030,6 +1134,9 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
             for (int s = 0; s < kStages; ++s)
                 if (ctl.last_fill[s] >= 0)
                     mbar_wait_bounded(&ctl.full[s], (uint32_t)(ctl.last_fill[s] / kStages) & 1u, &never, kWaitNs / 4);
+            for (int b = 0; b < 2; ++b)
+                if (ctl.last_q[b] >= 0)
+                    mbar_wait_bounded(&ctl.qt_full[b], (uint32_t)ctl.last_q[b] & 1u, &never, kWaitNs / 4);
             mbar_wait_bounded(&ctl.done, 0, &never, kWaitNs / 4);
             if (p.status)
                 atomicOr(p.status, SV_ATTN_TIMEOUT);
@@ -1057,18 +1164,18 @@ template <int D, int W> __global__ void __launch_bounds__(256) sv_attention_join
     const int R = tok * p.G + (hq - h * p.G), local = R - b * p.T * p.G;
     const int U = __ldg(&p.seg_start[p.B]), ub = __ldg(&p.seg_start[b]), ue = __ldg(&p.seg_start[b + 1]);
     const int C = min(grid, U);
-    const int nt = (ue - ub) / (p.H * p.nbs);
+    const int nt = (ue - ub) / (p.H * p.nbs) - kSegCost;
     const int rb = local / (2 * kTile), id_s = (b * p.H + h) * p.nbs + rb;
-    const int us = ub + (h * p.nbs + rb) * nt;
-    const int s0 = owner(us, U, C), s1 = owner(us + nt - 1, U, C);
+    const int us = ub + (h * p.nbs + rb) * (nt + kSegCost), ut = us + kSegCost;  // first unit, first tile's
+    const int s0 = owner(ut, U, C), s1 = owner(ut + nt - 1, U, C);
     if (p.UP == 0 && s0 == s1)
         return;  // written directly
     int id_p = 0, up = 0, p0 = 0, p1 = -1;
     if (p.UP > 0) {
         id_p = h * p.nbp + R / (2 * kTile);
-        up = id_p * p.ntp;
-        p0 = owner(up, U, C);
-        p1 = owner(up + p.ntp - 1, U, C);
+        up = id_p * (p.ntp + kSegCost);
+        p0 = owner(up + kSegCost, U, C);
+        p1 = owner(up + kSegCost + p.ntp - 1, U, C);
     }
     const int np = p1 - p0 + 1, n = np + (s1 - s0 + 1);
     // part i: its row of O, and (R, l)
@@ -1114,7 +1221,7 @@ template <int D, int W> __global__ void __launch_bounds__(256) sv_attention_join
         const float2 m = part(i, op);
         const float f = m.x == -INFINITY ? 0.0f : ex2(m.x - top);
         l += m.y != m.y ? m.y : f * m.y;
-        float o[E];
+        alignas(16) float o[E];
         if constexpr (E == 4)
             *reinterpret_cast<float4 *>(o) = *reinterpret_cast<const float4 *>(op + lane * 4);
         else
@@ -1174,9 +1281,10 @@ EncodeTiledFn encode_fn()
     return f;
 }
 
-// [B][n][heads][D] (strides in elements) as a map with boxes of 128 keys of one head: 64 bf16 or D codes wide.
+// [B][n][heads][D] (strides in elements) as a map with boxes of 128 keys of one head (or box_n tokens of box_heads
+// heads), 64 bf16 or D codes wide.
 bool make_map(CUtensorMap *m, const void *base, bool codes, int64_t B, int64_t n, int64_t heads, int64_t D, int64_t sb,
-              int64_t sn)
+              int64_t sn, int box_n = kTile, int box_heads = 1)
 {
     EncodeTiledFn enc = encode_fn();
     if (!enc)
@@ -1184,7 +1292,7 @@ bool make_map(CUtensorMap *m, const void *base, bool codes, int64_t B, int64_t n
     const cuuint64_t es = codes ? 1 : 2;
     const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)n, (cuuint64_t)B};
     const cuuint64_t strides[3] = {(cuuint64_t)D * es, (cuuint64_t)sn * es, (cuuint64_t)sb * es};
-    const cuuint32_t box[4] = {(cuuint32_t)(codes ? D : 64), 1, kTile, 1};
+    const cuuint32_t box[4] = {(cuuint32_t)(codes ? D : 64), (cuuint32_t)box_heads, (cuuint32_t)box_n, 1};
     const cuuint32_t estr[4] = {1, 1, 1, 1};
     return enc(m, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base),
                dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -1224,8 +1332,8 @@ bool plan(const sv_attention_args &a, Plan &w)
     w.ntp = (int)((a.prefix_len + kTile - 1) / kTile);
     w.nbp = (int)((rows + 2 * kTile - 1) / (2 * kTile));
     w.nbs = (int)((seq_rows + 2 * kTile - 1) / (2 * kTile));
-    w.UP = a.heads_kv * w.nbp * w.ntp;  // below 2^31 * 2^24
-    const int64_t tiles = (a.max_len + kTile - 1) / kTile + 1;
+    w.UP = a.prefix_len > 0 ? a.heads_kv * w.nbp * (w.ntp + kSegCost) : 0;  // below 2^31 * 2^24
+    const int64_t tiles = (a.max_len + kTile - 1) / kTile + 1 + kSegCost;
     if (w.UP > big / 2 || a.heads_kv * w.nbs > big || a.B * a.heads_kv * w.nbs > big || tiles > big / 2 / (a.B * a.heads_kv * w.nbs + 1))
         return false;
     w.most = w.UP + a.B * a.heads_kv * w.nbs * tiles;
@@ -1350,7 +1458,8 @@ extern "C" sv_status spec_verify_attention(const sv_attention_args *args, void *
     Plan w;
     // the tensor maps take strides below 2^40 bytes
     if (!plan(a, w) || a.max_len > (1ll << 38) / nrow || (a.B > 1 && a.new_stride_b > (1ll << 38)) ||
-        (a.T > 1 && a.new_stride_t > (1ll << 38)))
+        (a.T > 1 && a.new_stride_t > (1ll << 38)) || (a.B > 1 && a.q_stride_b > (1ll << 38)) ||
+        (a.T > 1 && a.q_stride_t > (1ll << 38)))
         return SV_ERR_TOO_LARGE;
     if (!a.workspace || a.workspace_bytes < w.bytes)
         return SV_ERR_INVALID_ARG;
@@ -1359,11 +1468,11 @@ extern "C" sv_status spec_verify_attention(const sv_attention_args *args, void *
         return SV_ERR_CUDA;
 
     Maps maps;
+    AttnParams p = {};
     const int D = (int)a.head_dim;
-    bool any = false, ok = true;
+    bool ok = true;
     auto map = [&](CUtensorMap *m, const void *base, bool codes, int64_t B, int64_t n, int64_t sb, int64_t sn) {
         ok = ok && make_map(m, base, codes, B, n, a.heads_kv, D, sb, sn);
-        any = true;
     };
     if (a.max_len > 0) {
         map(&maps.k, a.k_cache, e4, a.B, a.max_len, a.max_len * nrow, nrow);
@@ -1374,6 +1483,11 @@ extern "C" sv_status spec_verify_attention(const sv_attention_args *args, void *
         map(&maps.kn, a.k_new, false, a.B, a.T, sb, sn);
         map(&maps.vn, a.v_new, false, a.B, a.T, sb, sn);
     }
+    p.tma_q = a.T * w.G <= kTile;
+    if (p.tma_q) {  // box: one token range's rows of one head, 64 wide
+        const int64_t st_ = a.T > 1 ? a.q_stride_t : qrow, sb_ = a.B > 1 ? a.q_stride_b : a.T * st_;
+        ok = ok && make_map(&maps.q, a.q, false, a.B, a.T, a.heads_q, D, sb_, st_, (int)a.T, w.G);
+    }
     if (a.prefix_len > 0) {
         map(&maps.kp, a.k_prefix, e4, 1, a.prefix_len, a.prefix_len * nrow, nrow);
         map(&maps.vp, a.v_prefix, e4, 1, a.prefix_len, a.prefix_len * nrow, nrow);
@@ -1381,7 +1495,6 @@ extern "C" sv_status spec_verify_attention(const sv_attention_args *args, void *
     if (!ok)
         return SV_ERR_CUDA;
 
-    AttnParams p = {};
     p.q = static_cast<const __nv_bfloat16 *>(a.q);
     p.k_scale = a.k_scale;
     p.v_scale = a.v_scale;

@@ -106,6 +106,7 @@ struct AttnParams {
     float *lse;
     int32_t *status;
     int32_t *seg_start;     // [B + 1] first unit of each sequence, written for the joining kernel
+    int4 *cuts;             // [2 * CTAs] the segment that a CTA's stretch starts inside of, for the joining kernel
     float *whole_p, *whole_s, *pieces;  // partial results: whole prefix segments, whole segments, cut segments
     long long q_sb, q_st;
     int B, T, Hq, H, G, L, Lp;
@@ -471,6 +472,13 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
     Walk walk;
     walk.start(p, u0, u1, ctl.start_b, ctl.start_ub);
     Seg seg;
+    if (tid == 32 * 11 && p.UP == 0) {  // the idle warp
+        Walk w = walk;
+        const bool cut = w.next(p, seg) && seg.t0 > 0;
+        // its first tile's unit: the stretch starts at tile t0
+        p.cuts[2 * blockIdx.x] = make_int4(cut ? seg.row0 : -1, seg.nrows, u0 - seg.t0, seg.nt);
+        p.cuts[2 * blockIdx.x + 1] = make_int4(seg.h, 0, 0, 0);
+    }
 
     if (warp >= 8) {
     regs_dec<kRegsOther>();
@@ -537,119 +545,133 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
         }
         __syncwarp();
     } else if (warp == 9) {
-        // ---- MMA issuer ----
-        if (lane == 0) {
-            constexpr uint32_t idS = idesc_bf16_f32(kTile, kTile);
-            constexpr uint32_t idO = idesc_bf16_f32(kTile, D) | (1u << 16);
-            constexpr uint32_t idS8 = idesc_f8_f32(0, 0, kTile, kTile, 0);
-            constexpr uint32_t idO8 = idesc_f8_f32(1, 0, kTile, D, 1);
-            constexpr int kSw8 = D;             // an e4m3 row is D bytes: its swizzle
-            constexpr uint32_t kAtom8 = 8 * D;  // 8 rows of it
-            uint32_t base = 0;                  // ring fills before this segment
-            uint32_t nq = 0, npv[2] = {0, 0}, ntq = 0;
-            bool by_threads = false;
-            while (walk.next(p, seg)) {
-                if (seg.none())
-                    continue;
-                const bool pair = seg.pair(), draft = seg.draft();
-                const int njobs = pair ? 2 * seg.n : seg.n;
-                const uint32_t qb = seg.tq ? ntq & 1u : 0u;
-                if (seg.tq && ntq == 0 && by_threads) {
-                    tc_commit(&ctl.q_empty[0]);  // the earlier segments' products with Q
-                    tc_commit(&ctl.q_empty[1]);
-                }
-                if (seg.tq && (!E4 || draft))
-                    await(ctl, &ctl.qt_full[qb], ntq >> 1);
-                else
+        // ---- MMA issuer: the whole warp walks and waits, one elected lane issues; what the
+        // descriptors are made of is made uniform (the stage by a shuffle), so that they need
+        // no work per instruction ----
+        constexpr uint32_t idS = idesc_bf16_f32(kTile, kTile);
+        constexpr uint32_t idO = idesc_bf16_f32(kTile, D) | (1u << 16);
+        constexpr uint32_t idS8 = idesc_f8_f32(0, 0, kTile, kTile, 0);
+        constexpr uint32_t idO8 = idesc_f8_f32(1, 0, kTile, D, 1);
+        constexpr int kSw8 = D;             // an e4m3 row is D bytes: its swizzle
+        constexpr uint32_t kAtom8 = 8 * D;  // 8 rows of it
+        const uint64_t dQ = smem_desc_k128(smem), dK = smem_desc_k128(ring);
+        const uint64_t dV = smem_desc(ring, kPanel, 1024, 128);
+        const uint64_t dKV8 = smem_desc(ring, 16, kAtom8, kSw8);
+        const uint32_t tmu = __shfl_sync(0xffffffffu, tmem, 0);
+        const bool issue = elect_one();
+        uint32_t base = 0;                  // ring fills before this segment
+        uint32_t nq = 0, npv[2] = {0, 0}, ntq = 0;
+        bool by_threads = false;
+        while (walk.next(p, seg)) {
+            if (seg.none())
+                continue;
+            const bool pair = seg.pair(), draft = seg.draft();
+            const int njobs = pair ? 2 * seg.n : seg.n;
+            const uint32_t qb = seg.tq ? ntq & 1u : 0u;
+            if (seg.tq && ntq == 0 && by_threads && issue) {
+                tc_commit(&ctl.q_empty[0]);  // the earlier segments' products with Q
+                tc_commit(&ctl.q_empty[1]);
+            }
+            __syncwarp();
+            if (seg.tq && (!E4 || draft))
+                await(ctl, &ctl.qt_full[qb], ntq >> 1);
+            else
+                await(ctl, &ctl.q_full, nq++);
+            ntq += seg.tq;
+            by_threads |= !seg.tq;
+            bool q8 = E4 && !draft;
+            auto scores = [&](int q) {
+                const int i = pair ? q >> 1 : q, s = q & 1;
+                const bool dr = draft && i == 0;
+                if (E4 && !dr && !q8) {
                     await(ctl, &ctl.q_full, nq++);
-                ntq += seg.tq;
-                by_threads |= !seg.tq;
+                    q8 = true;
+                }
+                const uint32_t f = base + Fills<D, E4>::at(seg, i);
+                const uint32_t st = __shfl_sync(0xffffffffu, f % kStages, 0);
+                await(ctl, &ctl.full[st], f / kStages);
                 tc_fence_after();
-                bool q8 = E4 && !draft;
-                auto scores = [&](int q) {
-                    const int i = pair ? q >> 1 : q, s = q & 1;
-                    const bool dr = draft && i == 0;
-                    if (E4 && !dr && !q8) {
-                        await(ctl, &ctl.q_full, nq++);
-                        tc_fence_after();
-                        q8 = true;
-                    }
-                    const uint32_t f = base + Fills<D, E4>::at(seg, i);
-                    const int st = (int)(f % kStages);
-                    await(ctl, &ctl.full[st], f / kStages);
-                    tc_fence_after();
-                    const unsigned char *qt = smem + (pair ? s : qb) * C::kQTile, *kt = ring + st * kSlotBytes;
-                    const uint32_t d = tmem + 256 + 128 * s;
+                const uint32_t qs = __shfl_sync(0xffffffffu, pair ? (uint32_t)s : qb, 0);
+                const uint32_t d = tmu + 256 + 128 * __shfl_sync(0xffffffffu, s, 0);
+                const uint64_t q0 = dQ + qs * (uint32_t)(C::kQTile / 16);
+                if (issue) {
                     if (!E4 || dr) {
+                        const uint64_t k0 = dK + st * (uint32_t)(kSlotBytes / 16);
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk)
-                            tc_mma_bf16(d, smem_desc_k128(qt + kPanel * (kk / 4)) + 2u * (kk & 3),
-                                        smem_desc_k128(kt + kPanel * (kk / 4)) + 2u * (kk & 3), idS, kk != 0);
+                            tc_mma_bf16(d, q0 + (uint32_t)(kPanel / 16 * (kk / 4) + 2 * (kk & 3)),
+                                        k0 + (uint32_t)(kPanel / 16 * (kk / 4) + 2 * (kk & 3)), idS, kk != 0);
                     } else {
-                        const uint64_t dk = smem_desc(kt, 16, kAtom8, kSw8);
+                        const uint64_t k0 = dKV8 + st * (uint32_t)(kSlotBytes / 16);
 #pragma unroll
-                        for (int part = 0; part < 2; ++part) {
-                            // the second term: the next panel (D = 128), or the other half of the same rows
-                            const uint64_t dq = smem_desc_k128(qt + (D == 128 ? part * kPanel : 0)) + (D == 64 ? 4u * part : 0u);
+                        for (int part = 0; part < 2; ++part)  // the second term: the next panel (D = 128), or the other half of the same rows
 #pragma unroll
                             for (int kk = 0; kk < D / 32; ++kk)
-                                tc_mma_f8(d, dq + 2u * kk, dk + 2u * kk, idS8, part || kk);
-                        }
+                                tc_mma_f8(d, q0 + (uint32_t)(part * (D == 128 ? kPanel / 16 : 4) + 2 * kk), k0 + 2u * kk, idS8,
+                                          part || kk);
                     }
                     tc_commit(&ctl.s_full[s]);
                     if (seg.tq && q == njobs - 1)
                         tc_commit(&ctl.q_empty[qb]);
                     if (Fills<D, E4>::two(dr) && (!pair || s == 1))
                         tc_commit(&ctl.empty[st]);  // no later job reads these keys
-                };
-                auto product = [&](int q) {
-                    const int i = pair ? q >> 1 : q, s = q & 1;
-                    const bool dr = draft && i == 0, two = Fills<D, E4>::two(dr);
-                    const uint32_t f = base + Fills<D, E4>::at(seg, i) + (two ? 1 : 0);
-                    const int st = (int)(f % kStages);
-                    await(ctl, &ctl.full[st], f / kStages);
-                    if (dr || (!seg.prefix && seg.valid(seg.t0 + i) < kTile))
-                        await(ctl, &ctl.fix[st], f / kStages);
-                    if (dr && q == 0) {
-                        for (int w = 0; w < 4; ++w)
-                            ctl.poison[w] = ctl.poison_slot[st][w];
+                }
+                __syncwarp();
+            };
+            auto product = [&](int q) {
+                const int i = pair ? q >> 1 : q, s = q & 1;
+                const bool dr = draft && i == 0, two = Fills<D, E4>::two(dr);
+                const uint32_t f = base + Fills<D, E4>::at(seg, i) + (two ? 1 : 0);
+                const uint32_t st = __shfl_sync(0xffffffffu, f % kStages, 0);
+                await(ctl, &ctl.full[st], f / kStages);
+                if (dr || (!seg.prefix && seg.valid(seg.t0 + i) < kTile))
+                    await(ctl, &ctl.fix[st], f / kStages);
+                if (dr && q == 0) {
+                    if (lane < 4)
+                        ctl.poison[lane] = ctl.poison_slot[st][lane];
+                    __syncwarp();
+                    if (issue)
                         mbar_arrive(&ctl.poison_full);
-                    }
-                    await(ctl, &ctl.p_full[s], npv[s]++);
-                    tc_fence_after();
-                    const unsigned char *vt = ring + st * kSlotBytes + (two ? 0 : kVoff);
-                    const uint32_t d = tmem + 128 * s, a = tmem + 256 + 128 * s;
-                    const uint32_t acc = q >= 2;  // the slot's first job of the segment overwrites O
+                }
+                await(ctl, &ctl.p_full[s], npv[s]++);
+                tc_fence_after();
+                const uint32_t su = __shfl_sync(0xffffffffu, s, 0);
+                const uint32_t v = st * (uint32_t)(kSlotBytes / 16) + __shfl_sync(0xffffffffu, two ? 0u : (uint32_t)(kVoff / 16), 0);
+                const uint32_t d = tmu + 128 * su, a = tmu + 256 + 128 * su;
+                const uint32_t acc = q >= 2;  // the slot's first job of the segment overwrites O
+                if (issue) {
                     if (!E4 || dr) {
-                        const uint64_t dv = smem_desc(vt, kPanel, 1024, 128);
+                        const uint64_t v0 = dV + v;
 #pragma unroll
                         for (int kk = 0; kk < kTile / 16; ++kk)
-                            tc_mma_bf16_ts(d, a + 8 * kk, dv + (uint32_t)(kk * 16 * 128 / 16), idO, acc | (kk != 0));
+                            tc_mma_bf16_ts(d, a + 8 * kk, v0 + (uint32_t)(kk * 16 * 128 / 16), idO, acc | (kk != 0));
                     } else {
-                        const uint64_t dv = smem_desc(vt, 16, kAtom8, kSw8);
+                        const uint64_t v0 = dKV8 + v;
 #pragma unroll
                         for (int kk = 0; kk < kTile / 32; ++kk)
 #pragma unroll
                             for (int part = 0; part < 3; ++part)
-                                tc_mma_f8_ts(d, a + 24 * kk + 8 * part, dv + (uint32_t)(kk * 32 * D / 16), idO8,
+                                tc_mma_f8_ts(d, a + 24 * kk + 8 * part, v0 + (uint32_t)(kk * 32 * D / 16), idO8,
                                              acc | (kk != 0) | (part != 0));
                     }
                     tc_commit(&ctl.o_full[s]);
                     if (!pair || s == 1)
                         tc_commit(&ctl.empty[st]);
-                };
-                scores(0);
-                if (njobs > 1)
-                    scores(1);
-                for (int q = 0; q < njobs; ++q) {
-                    product(q);
-                    if (q + 2 < njobs)
-                        scores(q + 2);
                 }
-                base += Fills<D, E4>::at(seg, seg.n - 1) + (Fills<D, E4>::two(draft && seg.n == 1) ? 2 : 1);
+                __syncwarp();
+            };
+            scores(0);
+            if (njobs > 1)
+                scores(1);
+            for (int q = 0; q < njobs; ++q) {
+                product(q);
+                if (q + 2 < njobs)
+                    scores(q + 2);
             }
-            tc_commit(&ctl.done);
+            base += Fills<D, E4>::at(seg, seg.n - 1) + (Fills<D, E4>::two(draft && seg.n == 1) ? 2 : 1);
         }
+        if (issue)
+            tc_commit(&ctl.done);
         __syncwarp();
     } else if (warp == 10) {
         // ---- clearing warp: goes over every stage in order, so that a phase is never missed ----
@@ -1150,28 +1172,51 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
 
 // ---- joining the parts of cut rows -----------------------------------------------------
 
-// W warps per row (W = 8: a row's parts are dealt to the warps).
-template <int D, int W> __global__ void __launch_bounds__(256) sv_attention_join_kernel(AttnParams p, int grid)
+// W warps per row (W = 8: a row's parts are dealt to the warps).  With a prefix
+// every row has parts to join, and the grid goes over the rows; without one only
+// the segments that a stretch's end cuts do, and the grid's x goes over those ends.
+template <int D, int W, bool PREFIX> __global__ void __launch_bounds__(256) sv_attention_join_kernel(AttnParams p, int grid)
 {
     constexpr int E = D / 32;  // columns of a lane
     __shared__ float sh[W == 1 ? 1 : W * (D + 2)];
     grid_dependency_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long row = W == 1 ? (long long)blockIdx.x * 8 + warp : blockIdx.x;
-    if (row >= (long long)p.B * p.T * p.Hq)
-        return;
-    const int hq = (int)(row % p.Hq), tok = (int)(row / p.Hq), b = tok / p.T, h = hq / p.G;
-    const int R = tok * p.G + (hq - h * p.G), local = R - b * p.T * p.G;
-    const int U = __ldg(&p.seg_start[p.B]), ub = __ldg(&p.seg_start[b]), ue = __ldg(&p.seg_start[b + 1]);
+    const int U = __ldg(&p.seg_start[p.B]);
     const int C = min(grid, U);
-    const int nt = (ue - ub) / (p.H * p.nbs) - kSegCost;
-    const int rb = local / (2 * kTile), id_s = (b * p.H + h) * p.nbs + rb;
-    const int us = ub + (h * p.nbs + rb) * (nt + kSegCost), ut = us + kSegCost;  // first unit, first tile's
+    long long row;
+    int R, local, rb_row, us, ut, nt, id_s = 0, h;
+    if constexpr (PREFIX) {
+        row = W == 1 ? (long long)blockIdx.x * 8 + warp : blockIdx.x;
+        if (row >= (long long)p.B * p.T * p.Hq)
+            return;
+        const int hq = (int)(row % p.Hq), tok = (int)(row / p.Hq), b = tok / p.T;
+        h = hq / p.G;
+        R = tok * p.G + (hq - h * p.G);
+        local = R - b * p.T * p.G;
+        const int ub = __ldg(&p.seg_start[b]), ue = __ldg(&p.seg_start[b + 1]);
+        nt = (ue - ub) / (p.H * p.nbs) - kSegCost;
+        const int rb = local / (2 * kTile);
+        id_s = (b * p.H + h) * p.nbs + rb;
+        us = ub + (h * p.nbs + rb) * (nt + kSegCost);
+        ut = us + kSegCost;  // its first tile's unit
+        rb_row = local % (2 * kTile);
+    } else {
+        const int4 cut = __ldg(&p.cuts[2 * blockIdx.x]);
+        rb_row = W == 1 ? (int)blockIdx.y * 8 + warp : (int)blockIdx.y;
+        ut = cut.z;
+        nt = cut.w;
+        // one end of those that cut this segment does the work: the first
+        if (cut.x < 0 || rb_row >= cut.y || owner(ut, U, C) != (int)blockIdx.x - 1)
+            return;
+        h = __ldg(&p.cuts[2 * blockIdx.x + 1]).x;
+        us = ut - kSegCost;
+        R = cut.x + rb_row;
+        const int tok = R / p.G;
+        row = (long long)tok * p.Hq + h * p.G + (R - tok * p.G);
+    }
     const int s0 = owner(ut, U, C), s1 = owner(ut + nt - 1, U, C);
-    if (p.UP == 0 && s0 == s1)
-        return;  // written directly
     int id_p = 0, up = 0, p0 = 0, p1 = -1;
-    if (p.UP > 0) {
+    if constexpr (PREFIX) {
         id_p = h * p.nbp + R / (2 * kTile);
         up = id_p * (p.ntp + kSegCost);
         p0 = owner(up + kSegCost, U, C);
@@ -1192,7 +1237,7 @@ template <int D, int W> __global__ void __launch_bounds__(256) sv_attention_join
                 slot = p.pieces + (size_t)(2 * (p0 + i) + (stretch(p0 + i, U, C) >= up ? 0 : 1)) * nr * (D + 4);
             }
         } else {
-            rr = local % (2 * kTile);
+            rr = rb_row;
             if (s0 == s1) {
                 nr = p.rs;
                 slot = p.whole_s + (size_t)id_s * nr * (D + 4);
@@ -1319,7 +1364,7 @@ sv_status check(const sv_attention_args *a)
 struct Plan {
     int G, nbp, ntp, nbs, rp, rs, rm;
     int64_t UP, most;  // prefix units, units at full lengths
-    int64_t off_wp, off_ws, off_pc, bytes;
+    int64_t off_cut, off_wp, off_ws, off_pc, bytes;
 };
 
 bool plan(const sv_attention_args &a, Plan &w)
@@ -1342,6 +1387,8 @@ bool plan(const sv_attention_args &a, Plan &w)
     w.rm = a.prefix_len > 0 ? w.rp : w.rs;
     const int64_t per = (a.head_dim + 4) * 4;
     int64_t at = ((a.B + 1) * 4 + 1023) / 1024 * 1024;
+    w.off_cut = at;
+    at += (2 * kMaxCtas * 16 + 1023) / 1024 * 1024;
     w.off_wp = at;
     at += a.prefix_len > 0 ? a.heads_kv * w.nbp * w.rp * per : 0;
     at = (at + 1023) / 1024 * 1024;
@@ -1403,12 +1450,19 @@ template <int D, bool E4> sv_status launch(const Maps &maps, const AttnParams &p
     if (e == cudaSuccess) {
         // few rows: a CTA joins one row, its parts dealt to the warps
         const long long rows = (long long)p.B * p.T * p.Hq;
-        const bool wide = rows <= 1024;
-        cfg.gridDim = dim3((unsigned)(wide ? rows : (rows + 7) / 8));
         cfg.blockDim = dim3(256);
         cfg.dynamicSmemBytes = 0;
-        e = wide ? cudaLaunchKernelEx(&cfg, sv_attention_join_kernel<D, 8>, p, C)
-                 : cudaLaunchKernelEx(&cfg, sv_attention_join_kernel<D, 1>, p, C);
+        if (p.UP > 0) {
+            const bool wide = rows <= 1024;
+            cfg.gridDim = dim3((unsigned)(wide ? rows : (rows + 7) / 8));
+            e = wide ? cudaLaunchKernelEx(&cfg, sv_attention_join_kernel<D, 8, true>, p, C)
+                     : cudaLaunchKernelEx(&cfg, sv_attention_join_kernel<D, 1, true>, p, C);
+        } else {
+            const bool wide = p.rs <= 32;
+            cfg.gridDim = dim3((unsigned)C, (unsigned)(wide ? p.rs : (p.rs + 7) / 8));
+            e = wide ? cudaLaunchKernelEx(&cfg, sv_attention_join_kernel<D, 8, false>, p, C)
+                     : cudaLaunchKernelEx(&cfg, sv_attention_join_kernel<D, 1, false>, p, C);
+        }
     }
     if (e != cudaSuccess) {
         cudaGetLastError();
@@ -1507,6 +1561,7 @@ extern "C" sv_status spec_verify_attention(const sv_attention_args *args, void *
     p.status = a.status;
     unsigned char *ws = static_cast<unsigned char *>(a.workspace);
     p.seg_start = reinterpret_cast<int32_t *>(ws);
+    p.cuts = reinterpret_cast<int4 *>(ws + w.off_cut);
     p.whole_p = reinterpret_cast<float *>(ws + w.off_wp);
     p.whole_s = reinterpret_cast<float *>(ws + w.off_ws);
     p.pieces = reinterpret_cast<float *>(ws + w.off_pc);

@@ -11,6 +11,7 @@ SOURCES = [os.path.join(HERE, "csrc", "spec_verify.cu"), os.path.join(HERE, "csr
            os.path.join(HERE, "csrc", "lmhead.cu"), os.path.join(HERE, "csrc", "kv_path.cu"),
            os.path.join(HERE, "csrc", "attention.cu")]
 DEPENDS = SOURCES + [os.path.join(HERE, "csrc", "sv_device.cuh"), os.path.join(HERE, "csrc", "sv_tc.cuh"),
+                     os.path.join(HERE, "csrc", "attention_narrow.cuh"),
                      os.path.join(ROOT, "include", "spec_verify.h"),
                      os.path.join(ROOT, "include", "spec_verify_cache.h")]
 LIBRARY = os.path.join(HERE, "libspecverify.so")

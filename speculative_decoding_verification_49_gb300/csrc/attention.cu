@@ -122,6 +122,16 @@ struct Maps {
     CUtensorMap k, v, kn, vn, kp, vp, q;
 };
 
+// The producer walks; the other roles read each segment from a small ring, so that the
+// walk's divisions are in the kernel's code once (a role whose code leaves the instruction
+// cache pays memory latency for it at every segment).
+constexpr int kSegRing = 4;
+struct SegRing {
+    uint64_t full[kSegRing], empty[kSegRing];
+    alignas(16) int4 d[kSegRing][3];
+    int4 cur[2][3];  // what the softmax warps work on, handed out by one of them
+};
+
 template <bool E4> struct Tables {};
 template <> struct alignas(16) Tables<true> {  // read four keys at a time
     float kk[2][2][kTile];   // per slot, alternating: the key's factor of S
@@ -149,6 +159,7 @@ template <bool E4> struct Ctl {
     uint32_t tmem;
     int abort;
     int start_b, start_ub;
+    SegRing segs;
     float2 xch[2][kTile];         // (mu, l) of the slots' rows
     Tables<E4> tab;
 };
@@ -296,6 +307,35 @@ struct Walk {
     }
 };
 
+__device__ __forceinline__ void put_seg(int4 *d, const Seg &s, bool end)
+{
+    d[0] = make_int4((s.prefix ? 1 : 0) | (s.bad ? 2 : 0) | (s.tq ? 4 : 0) | (s.hn ? 8 : 0) | (s.first ? 16 : 0) | (end ? 32 : 0), s.b, s.h, s.row0);
+    d[1] = make_int4(s.nrows, s.t0, s.n, s.nt);
+    d[2] = make_int4(s.keys, s.rb, s.id, 0);
+}
+
+// False for the mark behind the last segment.
+__device__ __forceinline__ bool get_seg(const int4 *d, Seg &s)
+{
+    const int4 a = d[0], b = d[1], c = d[2];
+    s.prefix = a.x & 1;
+    s.bad = a.x & 2;
+    s.tq = a.x & 4;
+    s.hn = (a.x >> 3) & 1;
+    s.first = a.x & 16;
+    s.b = a.y;
+    s.h = a.z;
+    s.row0 = a.w;
+    s.nrows = b.x;
+    s.t0 = b.y;
+    s.n = b.z;
+    s.nt = b.w;
+    s.keys = c.x;
+    s.rb = c.y;
+    s.id = c.z;
+    return !(a.x & 32);
+}
+
 // Ring positions of a segment's tiles: a new tokens' tile (first) and every bf16 tile of D = 128 take two stages.
 template <int D, bool E4> struct Fills {
     __device__ static bool two(bool draft) { return Cfg<D, E4>::kTwo && (!E4 || draft); }
@@ -336,6 +376,34 @@ template <class C> __device__ __forceinline__ void await(C &ctl, uint64_t *bar, 
     }
 }
 
+// Next segment for a role of one warp; i counts its segments.  Ends it after a wait that gave up.
+template <class Ct> __device__ __forceinline__ bool next_seg(Ct &ctl, uint32_t &i, Seg &s)
+{
+    const uint32_t k = i % kSegRing;
+    await(ctl, &ctl.segs.full[k], i / kSegRing);
+    const bool more = get_seg(ctl.segs.d[k], s) && !*(volatile int *)&ctl.abort;
+    ++i;
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0)
+        mbar_arrive(&ctl.segs.empty[k]);
+    return __shfl_sync(0xffffffffu, (int)more, 0) != 0;
+}
+
+// One softmax thread takes the next segment for all of them; a barrier of theirs must follow
+// before they read it with get_seg(ctl.segs.cur[i & 1]) (i before this call).
+template <class Ct> __device__ __forceinline__ void hand_out_seg(Ct &ctl, uint32_t i)
+{
+    const uint32_t k = i % kSegRing;
+    await(ctl, &ctl.segs.full[k], i / kSegRing);
+    int4 a = ctl.segs.d[k][0];
+    if (*(volatile int *)&ctl.abort)
+        a.x |= 32;
+    ctl.segs.cur[i & 1][0] = a;
+    ctl.segs.cur[i & 1][1] = ctl.segs.d[k][1];
+    ctl.segs.cur[i & 1][2] = ctl.segs.d[k][2];
+    mbar_arrive(&ctl.segs.empty[k]);
+}
+
 __device__ __forceinline__ void bar_sync(int id, int threads)
 {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -348,8 +416,31 @@ __device__ __forceinline__ float nan_f()
 
 __device__ __forceinline__ unsigned pack_bf16(float lo, float hi)
 {
-    const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const unsigned *>(&r);
+    unsigned r;  // on plain registers: a cast of the vector types' address puts them into local memory
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t sub_f16(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Two f16 as two e5m2 (low half of the result).
+__device__ __forceinline__ uint32_t pack_e5m2(uint32_t a)
+{
+    uint16_t r;
+    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(a));
+    return r;
 }
 
 // (x0, x1) = (x0, x1) * (a0, a1) + (b0, b1) on float bits
@@ -357,6 +448,14 @@ __device__ __forceinline__ void fma_pair(uint32_t &x0, uint32_t &x1, float a0, f
 {
     float r0, r1;
     unpack2(fma2(pack2(__uint_as_float(x0), __uint_as_float(x1)), pack2(a0, a1), pack2(b0, b1)), r0, r1);
+    x0 = __float_as_uint(r0);
+    x1 = __float_as_uint(r1);
+}
+
+__device__ __forceinline__ void add_pair(uint32_t &x0, uint32_t &x1, float a0, float a1)
+{
+    float r0, r1;
+    unpack2(add2(pack2(__uint_as_float(x0), __uint_as_float(x1)), pack2(a0, a1)), r0, r1);
     x0 = __float_as_uint(r0);
     x1 = __float_as_uint(r1);
 }
@@ -370,6 +469,290 @@ __device__ __forceinline__ int code_exponent(unsigned m)
 __device__ __forceinline__ float pow2i(int e)
 {
     return __int_as_float((e + 127) << 23);
+}
+
+// ---- roles that both kernels share -------------------------------------------------
+
+// This CTA's stretch of the line of units, and the sequence that it starts in
+// (ctl.start_b, whose units begin at ctl.start_ub); CTA 0 writes the sequences'
+// first units.  All threads; ends with a barrier, as does what was set up before.
+template <int kThr, class Ct> __device__ __forceinline__ void find_stretch(const AttnParams &p, Ct &ctl, int &u0, int &u1)
+{
+    // ---- units of every sequence: this CTA's stretch and where it starts ----
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int per = p.H * p.nbs;  // segments of a sequence
+    const int chunk = cdiv(p.B, kThr);
+    const int bs = min(p.B, tid * chunk), be = min(p.B, bs + chunk);
+    int mine = 0;
+    for (int b = bs; b < be; ++b)
+        mine += (kSegCost + tiles_of(p, clean_len(p, raw_len(p, b)).n));
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o)
+            incl += x;
+    }
+    if (lane == 31)
+        ctl.warp_sum[warp] = incl;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    int before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < kThr / 32; ++w) {
+        const int x = ctl.warp_sum[w];
+        before += w < warp ? x : 0;
+        total += x;
+    }
+    const int U = p.UP + per * total;
+    // no more stretches than units: none is empty, the CTAs past them have nothing to do
+    const int nC = min((int)gridDim.x, U);
+    u0 = stretch(min((int)blockIdx.x, nC), U, nC);
+    u1 = stretch(min((int)blockIdx.x + 1, nC), U, nC);
+    {
+        int ub = p.UP + per * (before + incl - mine);
+        const int target = max(u0, p.UP);
+        const bool holds = target >= ub && target < ub + per * mine;
+        if (holds || blockIdx.x == 0)
+            for (int b = bs; b < be; ++b) {
+                const int next = ub + per * (kSegCost + tiles_of(p, clean_len(p, raw_len(p, b)).n));
+                if (target >= ub && target < next) {
+                    ctl.start_b = b;
+                    ctl.start_ub = ub;
+                }
+                if (blockIdx.x == 0)
+                    p.seg_start[b] = ub;
+                ub = next;
+            }
+        if (blockIdx.x == 0 && tid == 0)
+            p.seg_start[p.B] = U;
+    }
+    __syncthreads();
+}
+
+// Producer (one thread): walks the stretch and publishes its segments, Q by TMA where it comes that way, K and V tiles into the ring.
+template <int D, bool E4, int kStages, int kQBufs, int kQBytes, int kQPanel, class Ct>
+__device__ __forceinline__ void produce(const AttnParams &p, const Maps &maps, Ct &ctl, Walk walk, unsigned char *smem, unsigned char *ring)
+{
+    Seg seg;
+    uint32_t fill = 0;
+    auto acquire = [&](int &s) {
+        s = (int)(fill % kStages);
+        if (fill >= (uint32_t)kStages)
+            await(ctl, &ctl.empty[s], fill / kStages - 1);
+        return !*(volatile int *)&ctl.abort;
+    };
+    bool ok = true, by_threads = false, cut_known = false;
+    uint32_t ntq = 0, nseg = 0;
+    auto publish = [&](bool end) {
+        const uint32_t k = nseg % kSegRing;
+        if (nseg >= (uint32_t)kSegRing)
+            await(ctl, &ctl.segs.empty[k], nseg / kSegRing - 1);
+        if (*(volatile int *)&ctl.abort)
+            return false;
+        put_seg(ctl.segs.d[k], seg, end);
+        mbar_arrive(&ctl.segs.full[k]);
+        ++nseg;
+        return true;
+    };
+    while (ok) {
+        const bool more = walk.next(p, seg);
+        if (!cut_known && p.UP == 0) {
+            // the segment that this CTA's stretch starts inside of, for the joining kernel: the stretch starts at its tile t0
+            const bool cut = more && seg.t0 > 0;
+            p.cuts[2 * blockIdx.x] = make_int4(cut ? seg.row0 : -1, cut ? seg.nrows : 0, cut ? walk.u0 - seg.t0 : 0, cut ? seg.nt : 0);
+            p.cuts[2 * blockIdx.x + 1] = make_int4(cut ? seg.h : 0, 0, 0, 0);
+        }
+        cut_known = true;
+        if (!publish(!more) || !more)
+            break;
+        if (seg.none())
+            continue;
+        if (seg.tq) {
+            // the buffer was read last by the TMA segment kQBufs before, or by the segments whose Q came otherwise
+            const uint32_t qb = ntq % kQBufs, use = ntq / kQBufs + (by_threads ? 1 : 0);
+            if (use > 0)
+                await(ctl, &ctl.q_empty[qb], use - 1);
+            if (*(volatile int *)&ctl.abort)
+                break;
+            mbar_arrive_expect_tx(&ctl.qt_full[qb], (uint32_t)seg.nrows * D * 2);
+            for (int x = 0; x < D; x += 64)
+                tma_load_4d(smem + qb * kQBytes + (x / 64) * kQPanel, &maps.q, x, seg.h * p.G, 0, seg.b, &ctl.qt_full[qb]);
+            ctl.last_q[qb] = (int)(ntq / kQBufs);
+            ++ntq;
+        } else {
+            by_threads = true;
+        }
+        for (int i = 0; i < seg.n && ok; ++i) {
+            const int tile = seg.t0 + i;
+            const bool draft = seg.hn && tile == 0;
+            const CUtensorMap *mk = draft ? &maps.kn : seg.prefix ? &maps.kp : &maps.k;
+            const CUtensorMap *mv = draft ? &maps.vn : seg.prefix ? &maps.vp : &maps.v;
+            const int key = draft ? 0 : seg.key0(tile), b = seg.prefix ? 0 : seg.b;
+            int s;
+            if (Fills<D, E4>::two(draft)) {
+                for (int half = 0; half < 2 && ok; ++half) {
+                    if (!(ok = acquire(s)))
+                        break;
+                    unsigned char *dst = ring + s * kSlotBytes;
+                    const CUtensorMap *m = half ? mv : mk;
+                    mbar_arrive_expect_tx(&ctl.full[s], 2 * kPanel);
+                    tma_load_4d(dst, m, 0, seg.h, key, b, &ctl.full[s]);
+                    tma_load_4d(dst + kPanel, m, 64, seg.h, key, b, &ctl.full[s]);
+                    ctl.last_fill[s] = (int)fill++;
+                }
+            } else {
+                if (!(ok = acquire(s)))
+                    break;
+                unsigned char *dst = ring + s * kSlotBytes;
+                const uint32_t bytes = E4 && !draft ? kTile * D : kPanel;  // of K, of V
+                mbar_arrive_expect_tx(&ctl.full[s], 2 * bytes);
+                tma_load_4d(dst, mk, 0, seg.h, key, b, &ctl.full[s]);
+                tma_load_4d(dst + kVoff, mv, 0, seg.h, key, b, &ctl.full[s]);
+                ctl.last_fill[s] = (int)fill++;
+            }
+        }
+    }
+}
+
+// Clearing warp: goes over every stage in order, so that a phase is never missed.
+template <int D, bool E4, int kStages, class Ct>
+__device__ __forceinline__ void clear_values(const AttnParams &p, Ct &ctl, unsigned char *ring, int lane)
+{
+    Seg seg;
+    uint32_t fill = 0, iseg = 0;
+    while (next_seg(ctl, iseg, seg)) {
+        if (seg.none())
+            continue;
+        for (int i = 0; i < seg.n; ++i) {
+            const int tile = seg.t0 + i;
+            const bool draft = seg.hn && tile == 0, two = Fills<D, E4>::two(draft);
+            for (int part = two ? 0 : 1; part < 2; ++part, ++fill) {
+                const int st = (int)(fill % kStages);
+                await(ctl, &ctl.full[st], fill / kStages);
+                if (part == 1) {
+                    unsigned char *vt = ring + st * kSlotBytes + (two ? 0 : kVoff);
+                    if (draft) {
+                        uint32_t bits[4] = {0, 0, 0, 0};
+                        for (int c = lane; c < p.T * (D / 8); c += 32) {  // 16-byte pieces of the tokens' rows
+                            const int row = c / (D / 8), x = c % (D / 8);
+                            uint4 *a = reinterpret_cast<uint4 *>(vt + (x / 8) * kPanel + row * 128 + (x % 8) * 16);
+                            uint4 v = *a;
+                            uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                            bool bad = false;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                if ((w[k] & 0x7f80u) == 0x7f80u) {
+                                    w[k] &= 0xffff0000u;
+                                    bad = true;
+                                }
+                                if ((w[k] & 0x7f800000u) == 0x7f800000u) {
+                                    w[k] &= 0xffffu;
+                                    bad = true;
+                                }
+                            }
+                            if (bad) {
+                                *a = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    bits[k] |= (row >> 5) == k ? 1u << (row & 31) : 0u;
+                            }
+                        }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t all = __reduce_or_sync(0xffffffffu, bits[k]);
+                            if (lane == 0)
+                                ctl.poison_slot[st][k] = all;
+                        }
+                    } else if (!seg.prefix && seg.valid(tile) < kTile) {
+                        // rows behind the length: whatever the cache holds there must not count
+                        constexpr int kRow = E4 ? D : 128, kPanels = E4 ? 1 : D / 64;
+                        const int lo = seg.valid(tile) * kRow;
+                        for (int pn = 0; pn < kPanels; ++pn)
+                            for (int x = lo + lane * 16; x < kTile * kRow; x += 512)
+                                *reinterpret_cast<uint4 *>(vt + pn * kPanel + x) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_async_shared();
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&ctl.fix[st]);
+                    mbar_arrive(&ctl.empty[st]);
+                }
+            }
+        }
+    }
+}
+
+// End of a kernel: all threads.
+template <int kStages, int kQBufs, class Ct> __device__ __forceinline__ void finish(const AttnParams &p, Ct &ctl)
+{
+    tc_fence_before();
+    __syncthreads();
+    if (ctl.abort) {
+        // let what is in flight end before the CTA's memory goes
+        if (threadIdx.x == 0) {
+            int never = 0;
+            for (int s = 0; s < kStages; ++s)
+                if (ctl.last_fill[s] >= 0)
+                    mbar_wait_bounded(&ctl.full[s], (uint32_t)(ctl.last_fill[s] / kStages) & 1u, &never, kWaitNs / 4);
+            for (int b = 0; b < kQBufs; ++b)
+                if (ctl.last_q[b] >= 0)
+                    mbar_wait_bounded(&ctl.qt_full[b], (uint32_t)ctl.last_q[b] & 1u, &never, kWaitNs / 4);
+            mbar_wait_bounded(&ctl.done, 0, &never, kWaitNs / 4);
+            if (p.status)
+                atomicOr(p.status, SV_ATTN_TIMEOUT);
+        }
+        __syncthreads();
+    }
+}
+
+// Largest magnitude (15 bits) of the finite ones among 8 bf16.
+__device__ __forceinline__ unsigned finite_max(uint4 v)
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    unsigned m = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t lo = w[j] & 0x7fffu, hi = (w[j] >> 16) & 0x7fffu;
+        m = max(m, max(lo >= 0x7f80u ? 0u : lo, hi >= 0x7f80u ? 0u : hi));
+    }
+    return m;
+}
+
+// 8 bf16 times f as two e4m3 terms each: the nearest code, and what it leaves; NaN for what is not finite.
+__device__ __forceinline__ void two_terms(uint4 v, float f, uint2 &first, uint2 &second)
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t hi[2], lo[2];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float a = __uint_as_float(w[j] << 16), b = __uint_as_float(w[j] & 0xffff0000u);
+        a = (w[j] & 0x7f80u) == 0x7f80u ? nan_f() : a * f;
+        b = (w[j] & 0x7f800000u) == 0x7f800000u ? nan_f() : b * f;
+        const uint32_t ch = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+        const float2 back = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)ch, __NV_E4M3)));
+        const uint32_t cl = __nv_cvt_float2_to_fp8x2(make_float2(a - back.x, b - back.y), __NV_SATFINITE, __NV_E4M3);
+        hi[j >> 1] = (j & 1) ? hi[j >> 1] | (ch << 16) : ch;
+        lo[j >> 1] = (j & 1) ? lo[j >> 1] | (cl << 16) : cl;
+    }
+    first = make_uint2(hi[0], hi[1]);
+    second = make_uint2(lo[0], lo[1]);
+}
+
+// Four weights as three e5m2 terms each: w in f16, whose upper byte is an e5m2
+// number, the upper byte of what that leaves, and the rest rounded.
+__device__ __forceinline__ void three_terms(const float *w, uint32_t &t0, uint32_t &t1, uint32_t &t2)
+{
+    uint32_t a = pack_f16(w[0], w[1]), b = pack_f16(w[2], w[3]);
+    t0 = __byte_perm(a, b, 0x7531);
+    a = sub_f16(a, a & 0xff00ff00u);
+    b = sub_f16(b, b & 0xff00ff00u);
+    t1 = __byte_perm(a, b, 0x7531);
+    a = sub_f16(a, a & 0xff00ff00u);
+    b = sub_f16(b, b & 0xff00ff00u);
+    t2 = __byte_perm(pack_e5m2(a), pack_e5m2(b), 0x5410);
 }
 
 // ---- the kernel ------------------------------------------------------------------------
@@ -401,11 +784,16 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
             mbar_init(&ctl.p_full[s], 4);
             mbar_init(&ctl.o_full[s], 1);
             mbar_init(&ctl.qt_full[s], 1);
-            mbar_init(&ctl.q_empty[s], 1);
+            // the MMAs that read Q; e4m3: and every softmax warp's word that it has seen Q land, so that no phase passes it by
+            mbar_init(&ctl.q_empty[s], 1 + (E4 ? kSoftmaxThreads / 32 : 0));
         }
         mbar_init(&ctl.q_full, kSoftmaxThreads);
         mbar_init(&ctl.poison_full, 1);
         mbar_init(&ctl.done, 1);
+        for (int k = 0; k < kSegRing; ++k) {
+            mbar_init(&ctl.segs.full[k], 1);
+            mbar_init(&ctl.segs.empty[k], 3);  // the MMA issuer, the clearing warp and one softmax thread
+        }
         ctl.last_q[0] = ctl.last_q[1] = -1;
         ctl.abort = 0;
         ctl.qmax[0] = ctl.qmax[1] = 0;
@@ -419,129 +807,19 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
     }
     grid_dependency_wait();  // nothing above reads what an earlier kernel wrote
 
-    // ---- units of every sequence: this CTA's stretch and where it starts ----
-    const int per = p.H * p.nbs;  // segments of a sequence
-    const int chunk = cdiv(p.B, kThreads);
-    const int bs = min(p.B, tid * chunk), be = min(p.B, bs + chunk);
-    int mine = 0;
-    for (int b = bs; b < be; ++b)
-        mine += (kSegCost + tiles_of(p, clean_len(p, raw_len(p, b)).n));
-    int incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o)
-            incl += x;
-    }
-    if (lane == 31)
-        ctl.warp_sum[warp] = incl;
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    int before = 0, total = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-        const int x = ctl.warp_sum[w];
-        before += w < warp ? x : 0;
-        total += x;
-    }
-    const int U = p.UP + per * total;
-    // no more stretches than units: none is empty, the CTAs past them have nothing to do
-    const int nC = min((int)gridDim.x, U);
-    const int u0 = stretch(min((int)blockIdx.x, nC), U, nC), u1 = stretch(min((int)blockIdx.x + 1, nC), U, nC);
-    {
-        int ub = p.UP + per * (before + incl - mine);
-        const int target = max(u0, p.UP);
-        const bool holds = target >= ub && target < ub + per * mine;
-        if (holds || blockIdx.x == 0)
-            for (int b = bs; b < be; ++b) {
-                const int next = ub + per * (kSegCost + tiles_of(p, clean_len(p, raw_len(p, b)).n));
-                if (target >= ub && target < next) {
-                    ctl.start_b = b;
-                    ctl.start_ub = ub;
-                }
-                if (blockIdx.x == 0)
-                    p.seg_start[b] = ub;
-                ub = next;
-            }
-        if (blockIdx.x == 0 && tid == 0)
-            p.seg_start[p.B] = U;
-    }
-    __syncthreads();
+    int u0, u1;
+    find_stretch<kThreads>(p, ctl, u0, u1);
     const uint32_t tmem = ctl.tmem;
-    Walk walk;
-    walk.start(p, u0, u1, ctl.start_b, ctl.start_ub);
     Seg seg;
-    if (tid == 32 * 11 && p.UP == 0) {  // the idle warp
-        Walk w = walk;
-        const bool cut = w.next(p, seg) && seg.t0 > 0;
-        // its first tile's unit: the stretch starts at tile t0
-        p.cuts[2 * blockIdx.x] = make_int4(cut ? seg.row0 : -1, seg.nrows, u0 - seg.t0, seg.nt);
-        p.cuts[2 * blockIdx.x + 1] = make_int4(seg.h, 0, 0, 0);
-    }
 
     if (warp >= 8) {
     regs_dec<kRegsOther>();
     if (warp == 8) {
         // ---- producer ----
         if (lane == 0) {
-            uint32_t fill = 0;
-            auto acquire = [&](int &s) {
-                s = (int)(fill % kStages);
-                if (fill >= (uint32_t)kStages)
-                    await(ctl, &ctl.empty[s], fill / kStages - 1);
-                return !*(volatile int *)&ctl.abort;
-            };
-            bool ok = true, by_threads = false;
-            uint32_t ntq = 0;
-            while (ok && walk.next(p, seg)) {
-                if (seg.none())
-                    continue;
-                if (seg.tq) {
-                    // buffer j & 1 was read last by TMA segment j - 2, or by the segments whose Q came otherwise
-                    const uint32_t qb = ntq & 1u, use = (ntq >> 1) + (by_threads ? 1 : 0);
-                    if (use > 0)
-                        await(ctl, &ctl.q_empty[qb], use - 1);
-                    if (*(volatile int *)&ctl.abort)
-                        break;
-                    mbar_arrive_expect_tx(&ctl.qt_full[qb], (uint32_t)seg.nrows * D * 2);
-                    for (int x = 0; x < D; x += 64)
-                        tma_load_4d(smem + qb * C::kQTile + (x / 64) * kPanel, &maps.q, x, seg.h * p.G, 0, seg.b, &ctl.qt_full[qb]);
-                    ctl.last_q[qb] = (int)(ntq >> 1);
-                    ++ntq;
-                } else {
-                    by_threads = true;
-                }
-                for (int i = 0; i < seg.n && ok; ++i) {
-                    const int tile = seg.t0 + i;
-                    const bool draft = seg.hn && tile == 0;
-                    const CUtensorMap *mk = draft ? &maps.kn : seg.prefix ? &maps.kp : &maps.k;
-                    const CUtensorMap *mv = draft ? &maps.vn : seg.prefix ? &maps.vp : &maps.v;
-                    const int key = draft ? 0 : seg.key0(tile), b = seg.prefix ? 0 : seg.b;
-                    int s;
-                    if (Fills<D, E4>::two(draft)) {
-                        for (int half = 0; half < 2 && ok; ++half) {
-                            if (!(ok = acquire(s)))
-                                break;
-                            unsigned char *dst = ring + s * kSlotBytes;
-                            const CUtensorMap *m = half ? mv : mk;
-                            mbar_arrive_expect_tx(&ctl.full[s], 2 * kPanel);
-                            tma_load_4d(dst, m, 0, seg.h, key, b, &ctl.full[s]);
-                            tma_load_4d(dst + kPanel, m, 64, seg.h, key, b, &ctl.full[s]);
-                            ctl.last_fill[s] = (int)fill++;
-                        }
-                    } else {
-                        if (!(ok = acquire(s)))
-                            break;
-                        unsigned char *dst = ring + s * kSlotBytes;
-                        const uint32_t bytes = E4 && !draft ? kTile * D : kPanel;  // of K, of V
-                        mbar_arrive_expect_tx(&ctl.full[s], 2 * bytes);
-                        tma_load_4d(dst, mk, 0, seg.h, key, b, &ctl.full[s]);
-                        tma_load_4d(dst + kVoff, mv, 0, seg.h, key, b, &ctl.full[s]);
-                        ctl.last_fill[s] = (int)fill++;
-                    }
-                }
-            }
+            Walk walk;
+            walk.start(p, u0, u1, ctl.start_b, ctl.start_ub);
+            produce<D, E4, kStages, 2, C::kQTile, kPanel>(p, maps, ctl, walk, smem, ring);
         }
         __syncwarp();
     } else if (warp == 9) {
@@ -562,7 +840,8 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
         uint32_t base = 0;                  // ring fills before this segment
         uint32_t nq = 0, npv[2] = {0, 0}, ntq = 0;
         bool by_threads = false;
-        while (walk.next(p, seg)) {
+        uint32_t iseg = 0;
+        while (next_seg(ctl, iseg, seg)) {
             if (seg.none())
                 continue;
             const bool pair = seg.pair(), draft = seg.draft();
@@ -626,14 +905,14 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
                 await(ctl, &ctl.full[st], f / kStages);
                 if (dr || (!seg.prefix && seg.valid(seg.t0 + i) < kTile))
                     await(ctl, &ctl.fix[st], f / kStages);
-                if (dr && q == 0) {
+                await(ctl, &ctl.p_full[s], npv[s]++);
+                if (dr && q == 0) {  // only now: the last segment's has been read
                     if (lane < 4)
                         ctl.poison[lane] = ctl.poison_slot[st][lane];
                     __syncwarp();
                     if (issue)
                         mbar_arrive(&ctl.poison_full);
                 }
-                await(ctl, &ctl.p_full[s], npv[s]++);
                 tc_fence_after();
                 const uint32_t su = __shfl_sync(0xffffffffu, s, 0);
                 const uint32_t v = st * (uint32_t)(kSlotBytes / 16) + __shfl_sync(0xffffffffu, two ? 0u : (uint32_t)(kVoff / 16), 0);
@@ -674,69 +953,7 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
             tc_commit(&ctl.done);
         __syncwarp();
     } else if (warp == 10) {
-        // ---- clearing warp: goes over every stage in order, so that a phase is never missed ----
-        uint32_t fill = 0;
-        while (walk.next(p, seg)) {
-            if (seg.none())
-                continue;
-            for (int i = 0; i < seg.n; ++i) {
-                const int tile = seg.t0 + i;
-                const bool draft = seg.hn && tile == 0, two = Fills<D, E4>::two(draft);
-                for (int part = two ? 0 : 1; part < 2; ++part, ++fill) {
-                    const int st = (int)(fill % kStages);
-                    await(ctl, &ctl.full[st], fill / kStages);
-                    if (part == 1) {
-                        unsigned char *vt = ring + st * kSlotBytes + (two ? 0 : kVoff);
-                        if (draft) {
-                            uint32_t bits[4] = {0, 0, 0, 0};
-                            for (int c = lane; c < p.T * (D / 8); c += 32) {  // 16-byte pieces of the tokens' rows
-                                const int row = c / (D / 8), x = c % (D / 8);
-                                uint4 *a = reinterpret_cast<uint4 *>(vt + (x / 8) * kPanel + row * 128 + (x % 8) * 16);
-                                uint4 v = *a;
-                                uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                                bool bad = false;
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    if ((w[k] & 0x7f80u) == 0x7f80u) {
-                                        w[k] &= 0xffff0000u;
-                                        bad = true;
-                                    }
-                                    if ((w[k] & 0x7f800000u) == 0x7f800000u) {
-                                        w[k] &= 0xffffu;
-                                        bad = true;
-                                    }
-                                }
-                                if (bad) {
-                                    *a = make_uint4(w[0], w[1], w[2], w[3]);
-#pragma unroll
-                                    for (int k = 0; k < 4; ++k)
-                                        bits[k] |= (row >> 5) == k ? 1u << (row & 31) : 0u;
-                                }
-                            }
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const uint32_t all = __reduce_or_sync(0xffffffffu, bits[k]);
-                                if (lane == 0)
-                                    ctl.poison_slot[st][k] = all;
-                            }
-                        } else if (!seg.prefix && seg.valid(tile) < kTile) {
-                            // rows behind the length: whatever the cache holds there must not count
-                            constexpr int kRow = E4 ? D : 128, kPanels = E4 ? 1 : D / 64;
-                            const int lo = seg.valid(tile) * kRow;
-                            for (int pn = 0; pn < kPanels; ++pn)
-                                for (int x = lo + lane * 16; x < kTile * kRow; x += 512)
-                                    *reinterpret_cast<uint4 *>(vt + pn * kPanel + x) = make_uint4(0, 0, 0, 0);
-                        }
-                        fence_async_shared();
-                    }
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(&ctl.fix[st]);
-                        mbar_arrive(&ctl.empty[st]);
-                    }
-                }
-            }
-        }
+        clear_values<D, E4, kStages>(p, ctl, ring, lane);
     }
     } else {
         regs_inc<kRegsSoftmax>();
@@ -748,7 +965,13 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
         uint32_t nj = 0, npois = 0;  // jobs of the slot, segments with new tokens so far
         uint32_t ntab = 0;           // e4m3 tiles of the slot so far
         uint32_t ntq = 0;            // segments whose Q came by TMA
-        while (walk.next(p, seg)) {
+        bool by_threads = false;     // earlier ones came otherwise
+        uint32_t iseg = 0;
+        if (tid == 0)
+            hand_out_seg(ctl, 0);
+        bar_sync(1, kSoftmaxThreads);
+        while (get_seg(ctl.segs.cur[iseg & 1], seg)) {
+            ++iseg;
             const bool pair = seg.pair(), draft = seg.draft(), none = seg.none();
             const int njobs = none ? 0 : pair ? 2 * seg.n : seg.n;
             const int rows = seg.slot_rows(s);
@@ -773,13 +996,7 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
                 for (int e = q_from; e < q_end; e += q_step) {
                     if (e >= rows * kPc)  // behind the rows: whatever the buffer held
                         continue;
-                    const uint4 v = *q_piece(e / kPc, e % kPc);
-                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t lo = w[j] & 0x7fffu, hi = (w[j] >> 16) & 0x7fffu;
-                        qm = max(qm, max(lo >= 0x7f80u ? 0u : lo, hi >= 0x7f80u ? 0u : hi));
-                    }
+                    qm = max(qm, finite_max(*q_piece(e / kPc, e % kPc)));
                 }
                 qm = __reduce_max_sync(0xffffffffu, qm);
                 if (lane == 0)
@@ -792,24 +1009,13 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
                 for (int e = q_from; e < q_end; e += q_step) {  // a warp holds whole rows
                     const int row = e / kPc, x0 = e % kPc;
                     const uint4 x = *q_piece(row, x0);
-                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                    uint32_t hi[2], lo[2];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float a = __uint_as_float(w[j] << 16), b = __uint_as_float(w[j] & 0xffff0000u);
-                        a = (w[j] & 0x7f80u) == 0x7f80u ? nan_f() : a * f;
-                        b = (w[j] & 0x7f800000u) == 0x7f800000u ? nan_f() : b * f;
-                        const uint32_t ch = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-                        const float2 back = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)ch, __NV_E4M3)));
-                        const uint32_t cl = __nv_cvt_float2_to_fp8x2(make_float2(a - back.x, b - back.y), __NV_SATFINITE, __NV_E4M3);
-                        hi[j >> 1] = (j & 1) ? hi[j >> 1] | (ch << 16) : ch;
-                        lo[j >> 1] = (j & 1) ? lo[j >> 1] | (cl << 16) : cl;
-                    }
+                    uint2 hi, lo;
+                    two_terms(x, f, hi, lo);
                     __syncwarp();
                     // 8 codes at byte 8 * x0 of a 128-byte row (D = 64: the second terms at byte 64 of it)
                     auto at = [&](int byte) { return qt + row * 128 + ((((byte >> 4) ^ (row & 7)) << 4) | (byte & 8)); };
-                    *reinterpret_cast<uint2 *>(at(8 * x0)) = make_uint2(hi[0], hi[1]);
-                    *reinterpret_cast<uint2 *>(D == 128 ? at(8 * x0) + kPanel : at(8 * x0 + 64)) = make_uint2(lo[0], lo[1]);
+                    *reinterpret_cast<uint2 *>(at(8 * x0)) = hi;
+                    *reinterpret_cast<uint2 *>(D == 128 ? at(8 * x0) + kPanel : at(8 * x0 + 64)) = lo;
                 }
                 fence_async_shared();
                 mbar_arrive(&ctl.q_full);
@@ -830,9 +1036,18 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
                         *q_piece(row, x) = v;
                     }
                 }
-                if (seg.tq && E4)
+                if (seg.tq && E4) {
+                    if (ntq == 0 && by_threads && lane == 0) {  // the earlier segments' part of the first phase
+                        mbar_arrive(&ctl.q_empty[0]);
+                        mbar_arrive(&ctl.q_empty[1]);
+                    }
                     await(ctl, &ctl.qt_full[qb], ntq >> 1);
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&ctl.q_empty[qb]);
+                }
                 ntq += seg.tq;
+                by_threads |= !seg.tq;
                 if (!E4 || draft) {
                     if (!seg.tq) {
                         fence_async_shared();
@@ -1017,19 +1232,7 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
                                 const float4 v = inv4[k / 4];
                                 la = fma2(pack2(w[0], w[1]), pack2(v.x, v.y), la);
                                 lb = fma2(pack2(w[2], w[3]), pack2(v.z, v.w), lb);
-                                // three e5m2 terms of f16 weights: the upper bytes of w, of w - first, of the rest
-                                __half2 ha = __floats2half2_rn(w[0], w[1]), hb = __floats2half2_rn(w[2], w[3]);
-#pragma unroll
-                                for (int part = 0; part < 2; ++part) {
-                                    const uint32_t ua = *reinterpret_cast<uint32_t *>(&ha), ub = *reinterpret_cast<uint32_t *>(&hb);
-                                    t8[8 * part + (k >> 2)] = __byte_perm(ua, ub, 0x7531);
-                                    const uint32_t ta = ua & 0xff00ff00u, tb2 = ub & 0xff00ff00u;
-                                    ha = __hsub2(ha, *reinterpret_cast<const __half2 *>(&ta));
-                                    hb = __hsub2(hb, *reinterpret_cast<const __half2 *>(&tb2));
-                                }
-                                const uint32_t ca = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(ha), __NV_SATFINITE, __NV_E5M2);
-                                const uint32_t cb = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(hb), __NV_SATFINITE, __NV_E5M2);
-                                t8[16 + (k >> 2)] = ca | (cb << 16);
+                                three_terms(w, t8[k >> 2], t8[8 + (k >> 2)], t8[16 + (k >> 2)]);
                             }
                             tmem_st16(tS + (c0 >> 5) * 24, t8);
                             tmem_st8(tS + (c0 >> 5) * 24 + 16, t8 + 16);
@@ -1143,32 +1346,23 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
             tc_fence_before();
             if (E4 && pt == 0)
                 ctl.qmax[s] = 0;  // read last before this segment's products
+            if (tid == 0)
+                hand_out_seg(ctl, iseg);
             bar_sync(1, kSoftmaxThreads);  // O has been read by both slots, the exchange may be overwritten
             tc_fence_after();
         }
     }
-    tc_fence_before();
-    __syncthreads();
-    if (ctl.abort) {
-        // let what is in flight end before the CTA's memory goes
-        if (tid == 0) {
-            int never = 0;
-            for (int s = 0; s < kStages; ++s)
-                if (ctl.last_fill[s] >= 0)
-                    mbar_wait_bounded(&ctl.full[s], (uint32_t)(ctl.last_fill[s] / kStages) & 1u, &never, kWaitNs / 4);
-            for (int b = 0; b < 2; ++b)
-                if (ctl.last_q[b] >= 0)
-                    mbar_wait_bounded(&ctl.qt_full[b], (uint32_t)ctl.last_q[b] & 1u, &never, kWaitNs / 4);
-            mbar_wait_bounded(&ctl.done, 0, &never, kWaitNs / 4);
-            if (p.status)
-                atomicOr(p.status, SV_ATTN_TIMEOUT);
-        }
-        __syncthreads();
-    }
+    finish<kStages, 2>(p, ctl);
     tc_fence_after();
     if (warp == 9)
         tmem_dealloc(tmem, kTmemCols);
 }
+
+} // namespace
+
+#include "attention_narrow.cuh"
+
+namespace {
 
 // ---- joining the parts of cut rows -----------------------------------------------------
 
@@ -1406,10 +1600,17 @@ bool al16(const void *p)
     return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
 }
 
-template <int D, bool E4> cudaError_t set_attr()
+template <int D> cudaError_t set_attr()
 {
-    return cudaFuncSetAttribute(sv_attention_kernel<D, E4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)smem_bytes<D, E4>());
+    const void *kernels[3] = {(const void *)sv_attention_kernel<D, false>, (const void *)sv_attention_kernel<D, true>,
+                              (const void *)sv_attention_narrow_kernel<D>};
+    const size_t bytes[3] = {smem_bytes<D, false>(), smem_bytes<D, true>(), narrow_smem<D>()};
+    for (int i = 0; i < 3; ++i) {
+        const cudaError_t e = cudaFuncSetAttribute(kernels[i], cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes[i]);
+        if (e != cudaSuccess)
+            return e;
+    }
+    return cudaSuccess;
 }
 
 // Function attributes and the SM count, once per device.
@@ -1425,8 +1626,8 @@ int device_sms()
     int n = sms[dev].load();
     if (n > 0)
         return n;
-    if (set_attr<64, false>() != cudaSuccess || set_attr<64, true>() != cudaSuccess || set_attr<128, false>() != cudaSuccess ||
-        set_attr<128, true>() != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) {
+    if (set_attr<64>() != cudaSuccess || set_attr<128>() != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) {
         cudaGetLastError();
         return 0;
     }
@@ -1441,12 +1642,20 @@ template <int D, bool E4> sv_status launch(const Maps &maps, const AttnParams &p
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)C);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem_bytes<D, E4>();
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, sv_attention_kernel<D, E4>, maps, p);
+    cudaError_t e;
+    // 8-bit caches, few rows and no prefix: the products turned around (attention_narrow.cuh)
+    if (E4 && p.UP == 0 && p.T * p.G <= kNarrowRows) {
+        cfg.blockDim = dim3(kNarrowThreads);
+        cfg.dynamicSmemBytes = narrow_smem<D>();
+        e = cudaLaunchKernelEx(&cfg, sv_attention_narrow_kernel<D>, maps, p);
+    } else {
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = smem_bytes<D, E4>();
+        e = cudaLaunchKernelEx(&cfg, sv_attention_kernel<D, E4>, maps, p);
+    }
     if (e == cudaSuccess) {
         // few rows: a CTA joins one row, its parts dealt to the warps
         const long long rows = (long long)p.B * p.T * p.Hq;

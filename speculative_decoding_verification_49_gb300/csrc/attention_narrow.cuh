@@ -1,0 +1,707 @@
+// attention_narrow.cuh -- the attention of attention.cu over e4m3 caches for
+// sequences of at most 64 (token, query head) rows a key/value head and no shared
+// prefix: single tokens and chains of a few drafts.
+//
+// With 8-bit keys and values a tile's HBM time halves, and the products of
+// attention.cu (rows on the tensor cores' M side, padded to 128) take longer than
+// that.  Here they are turned around: S^T = K Q^T puts a tile's 128 keys on M and the
+// rows on N = 64, and O^T = V^T P^T the head's channels on M.  That halves
+// the matrix work, the softmax uses all lanes whatever the number of rows
+// (thread = key), a key's scales are registers instead of table reads, and the
+// mask of the length is a property of the thread.  What it costs: a row's maximum
+// lies across threads.  It is not looked for: a reference only has to keep the weights
+// inside their range, so the first tile's is taken from the scores of four keys, and
+// each later tile is compared with it (one vote of the warpgroup); only when a score is beyond what the range
+// absorbs are the true maxima reduced and l and O^T rescaled.  l is summed over the
+// threads once, at the segment's end.
+//
+// P^T goes to shared memory (the B operand cannot come from tensor memory) as three
+// e5m2 terms side by side along N, so that one instruction of N = 192 reads V once
+// for all three; O^T is then the sum of three column ranges.  The two e4m3 terms
+// of Q add up in place.  Shared-memory traffic of a tile (128 keys of D = 128; the limit
+// is 128 B a cycle): 32 KB by TMA, 48 + 40 read by the products, 24 of P: 1150 cycles
+// against 1400 of HBM time.
+//
+// Four warpgroups do the softmax, each of 16 rows (those behind the last row idle), on
+// every tile: few enough values for a thread that none is spilled.  S^T and P^T are double, so
+// that the products of one tile run beside the softmax of the next; O^T is single.
+//   warps 0-15   warpgroup g: rows 16 g ..; thread = key, then channel
+//   warps 16-19  producer, MMA issuer, clearing warp, as in attention.cu; the keys' scales into shared memory
+// TMEM: O^T at column 0 (three parts of 64), S^T at 256 and 320.
+// Walk, ring, stretches, clearing and joining are attention.cu's.
+#pragma once
+
+namespace {
+
+constexpr int kNarrowRows = 64, kNarrowStages = 4;
+constexpr int kNarrowPanel = kNarrowRows * 128;  // 64 rows of 128 bytes of Q
+constexpr int kNarrowSoftmax = 512, kNarrowThreads = 640;
+// 640 threads start with 96 registers; the 512 softmax threads take 104, the others keep 64
+constexpr int kNarrowRegsStart = 96, kNarrowRegsSoftmax = 104, kNarrowRegsOther = 64;
+static_assert(kNarrowSoftmax * kNarrowRegsSoftmax + (kNarrowThreads - kNarrowSoftmax) * kNarrowRegsOther <=
+                  kNarrowThreads * kNarrowRegsStart, "the split is covered by what the launch holds");
+// The weights' range: a row's largest is at most 2^(base + slack) = 2^15 (e5m2 and f16 end above it); the first reference
+// is 2^margin above the best of four keys.  e5m2's smallest step, 2^-16, is then at most 2^-20 of the row's largest weight.
+constexpr float kNarrowBase = 8.0f, kNarrowSlack = 7.0f, kNarrowMargin = 4.0f;
+
+template <int D> struct NarrowCfg {
+    static constexpr int kQ = kNarrowRows * D * 2;      // Q in bf16
+    static constexpr int kQC = kNarrowRows * D * 2;     // its codes: the first terms' rows, then the second's
+    static constexpr int kTerm = kTile * kNarrowRows;   // one term of a slot's weights
+    static constexpr int kP = 3 * kTerm;
+};
+
+struct NarrowCtl {
+    uint64_t full[kNarrowStages], empty[kNarrowStages], fix[kNarrowStages];
+    uint64_t s_full[2], p_full[2], o_full[2];
+    uint64_t q_full;                 // Q's codes are written
+    uint64_t qt_full[1], q_empty[1]; // Q in bf16 has landed; no one reads it any more
+    uint64_t poison_full, done;
+    uint32_t poison_slot[kNarrowStages][4];
+    uint32_t poison[4];
+    unsigned qmax[2];                // alternating by conversion
+    int warp_sum[kNarrowThreads / 32];
+    int last_fill[kNarrowStages], last_q[1];
+    uint32_t tmem;
+    int abort;
+    int start_b, start_ub;
+    SegRing segs;
+    // per row
+    alignas(16) float nmu[kNarrowRows];      // base - mu
+    alignas(16) float fac[kNarrowRows];      // the last move of the reference; at the end the row's factor
+    alignas(16) float part[4][4][16];        // per warpgroup and warp: sampled scores, maxima, sums of its rows
+    float mu[kNarrowRows];
+    uint16_t scale[kNarrowStages][kTile];    // of a stage's keys: K's scale byte, V's in the upper half
+};
+
+template <int D> constexpr size_t narrow_smem()
+{
+    using N = NarrowCfg<D>;
+    return (size_t)N::kQ + N::kQC + 2 * (size_t)N::kP + (size_t)kNarrowStages * kSlotBytes + sizeof(NarrowCtl);
+}
+static_assert(narrow_smem<128>() <= 232448, "227 KiB of shared memory per CTA");
+
+// Order-preserving map of floats to ints (a positive NaN is above everything).
+__device__ __forceinline__ int ordered(float x)
+{
+    const int i = __float_as_int(x);
+    return i ^ ((i >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float unordered(int i)
+{
+    return __int_as_float(i ^ ((i >> 31) & 0x7fffffff));
+}
+
+// Whether any of the 128 threads of named barrier `id` has x.
+__device__ __forceinline__ bool any128(int id, bool x)
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.or.pred q, %2, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)x), "r"(id)
+        : "memory");
+    return r != 0;
+}
+
+// Sums 16 values over the warp: lanes i and i + 16 return the total of v[i].
+__device__ __forceinline__ float transpose_sum16(float *v, int lane)
+{
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+        v[k] += __shfl_xor_sync(0xffffffffu, v[k], 16);
+#pragma unroll
+    for (int o = 8; o >= 1; o >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int k = 0; k < o; ++k) {
+            const float give = up ? v[k] : v[k + o];
+            const float keep = up ? v[k + o] : v[k];
+            v[k] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+        }
+    }
+    return v[0];
+}
+
+template <int D>
+__global__ void __launch_bounds__(kNarrowThreads, 1) sv_attention_narrow_kernel(const __grid_constant__ Maps maps, AttnParams p)
+{
+    using N = NarrowCfg<D>;
+    constexpr int kStages = kNarrowStages;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    unsigned char *qc = smem + N::kQ, *pw = qc + N::kQC, *ring = pw + 2 * N::kP;
+    NarrowCtl &ctl = *reinterpret_cast<NarrowCtl *>(ring + kStages * kSlotBytes);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rows = p.T * p.G;  // of every segment, at most 64
+    const int ngroup = (rows + 15) / 16;
+
+    if (smem_u32(smem) & 1023u) {
+        if (tid == 0 && p.status)
+            atomicOr(p.status, SV_ATTN_TIMEOUT);
+        return;
+    }
+    if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&ctl.full[s], 2);  // the producer and the scales' warp
+            mbar_init(&ctl.empty[s], 2);
+            mbar_init(&ctl.fix[s], 1);
+            ctl.last_fill[s] = -1;
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&ctl.s_full[s], 1);
+            mbar_init(&ctl.p_full[s], 4 * ngroup);  // the warps that have rows
+            mbar_init(&ctl.o_full[s], 1);
+        }
+        mbar_init(&ctl.qt_full[0], 1);
+        // the MMAs that read Q, and every softmax warp's word that it has seen Q land: no phase may pass it by
+        mbar_init(&ctl.q_empty[0], 1 + kNarrowSoftmax / 32);
+        mbar_init(&ctl.q_full, kNarrowSoftmax);
+        mbar_init(&ctl.poison_full, 1);
+        mbar_init(&ctl.done, 1);
+        for (int k = 0; k < kSegRing; ++k) {
+            mbar_init(&ctl.segs.full[k], 1);
+            mbar_init(&ctl.segs.empty[k], 4);  // the MMA issuer, the clearing and the scales' warp, one softmax thread
+        }
+        ctl.last_q[0] = -1;
+        ctl.abort = 0;
+        ctl.qmax[0] = ctl.qmax[1] = 0;
+        ctl.start_b = 0;
+        ctl.start_ub = 0;
+        fence_mbar_init();
+    }
+    // rows of Q (and its codes) past the last one stay zero: TMA and the conversion write only rows that are there
+    for (int x = tid * 16; x < N::kQ + N::kQC; x += kNarrowThreads * 16)
+        *reinterpret_cast<uint4 *>(smem + x) = make_uint4(0, 0, 0, 0);
+    fence_async_shared();
+    if (warp == 17) {
+        tmem_alloc(&ctl.tmem, kTmemCols);
+        tmem_relinquish();
+    }
+    grid_dependency_wait();
+
+    int u0, u1;
+    find_stretch<kNarrowThreads>(p, ctl, u0, u1);
+    const uint32_t tmem = ctl.tmem;
+    Seg seg;
+
+    if (warp >= 16) {
+        regs_dec<kNarrowRegsOther>();
+        if (warp == 16) {
+            if (lane == 0) {
+                Walk walk;
+                walk.start(p, u0, u1, ctl.start_b, ctl.start_ub);
+                produce<D, true, kStages, 1, N::kQ, kNarrowPanel>(p, maps, ctl, walk, smem, ring);
+            }
+            __syncwarp();
+        } else if (warp == 17) {
+            // ---- MMA issuer ----
+            constexpr uint32_t kTr = (1u << 15) | (1u << 16);  // both operands MN-major
+            constexpr uint32_t idS = idesc_bf16_f32(kTile, kNarrowRows), idO = idS | kTr;
+            constexpr uint32_t idS8 = idesc_f8_f32(0, 0, kTile, kNarrowRows, 0);
+            constexpr uint32_t idO8 = idesc_f8_f32(0, 1, kTile, 3 * kNarrowRows, 0) | kTr;
+            constexpr int kSw8 = D;
+            constexpr uint32_t kAtom8 = 8 * D;
+            const uint64_t dQ = smem_desc_k128(smem), dQ8 = smem_desc(qc, 16, kAtom8, kSw8);
+            const uint64_t dK = smem_desc_k128(ring), dK8 = smem_desc(ring, 16, kAtom8, kSw8);
+            // V^T: M = 128 channels; with D = 64 the second 64 repeat the first (stride 0) and are not read
+            const uint64_t dV = smem_desc(ring, D == 128 ? kPanel : 0, 1024, 128);
+            const uint64_t dV8 = smem_desc(ring, D == 128 ? 16 : 0, kAtom8, kSw8);
+            const uint64_t dP = smem_desc(pw, 16, 1024, 128), dP8 = smem_desc(pw, N::kTerm, 512, 64);
+            const uint32_t tmu = __shfl_sync(0xffffffffu, tmem, 0);
+            const bool issue = elect_one();
+            uint32_t base = 0, nq = 0, nj = 0, nseg = 0, iseg = 0;
+            while (next_seg(ctl, iseg, seg)) {
+                if (seg.none())
+                    continue;
+                const bool draft = seg.draft();
+                const int njobs = seg.n;
+                if (draft)
+                    await(ctl, &ctl.qt_full[0], nseg);
+                ++nseg;
+                bool q8 = false;
+                auto scores = [&](int q) {
+                    const uint32_t s = (nj + (uint32_t)q) & 1u;
+                    const bool dr = draft && q == 0, first8 = !dr && !q8;
+                    if (first8) {
+                        await(ctl, &ctl.q_full, nq++);
+                        q8 = true;
+                    }
+                    const uint32_t f = base + Fills<D, true>::at(seg, q);
+                    const uint32_t st = __shfl_sync(0xffffffffu, f % kStages, 0);
+                    await(ctl, &ctl.full[st], f / kStages);
+                    tc_fence_after();
+                    const uint32_t d = tmu + 256 + 64 * __shfl_sync(0xffffffffu, s, 0);
+                    if (issue) {
+                        if (dr) {
+                            const uint64_t k0 = dK + st * (uint32_t)(kSlotBytes / 16);
+#pragma unroll
+                            for (int kk = 0; kk < D / 16; ++kk)
+                                tc_mma_bf16(d, k0 + (uint32_t)(kPanel / 16 * (kk / 4) + 2 * (kk & 3)),
+                                            dQ + (uint32_t)(kNarrowPanel / 16 * (kk / 4) + 2 * (kk & 3)), idS, kk != 0);
+                        } else {
+                            const uint64_t k0 = dK8 + st * (uint32_t)(kSlotBytes / 16);
+#pragma unroll
+                            for (int part = 0; part < 2; ++part)
+#pragma unroll
+                                for (int kk = 0; kk < D / 32; ++kk)
+                                    tc_mma_f8(d, k0 + 2u * kk, dQ8 + (uint32_t)(part * kNarrowRows * D / 16 + 2 * kk), idS8,
+                                              part || kk);
+                        }
+                        tc_commit(&ctl.s_full[s]);
+                        if (first8 || (dr && njobs == 1))
+                            tc_commit(&ctl.q_empty[0]);  // the codes are made and the new tokens' product is ahead of this
+                        if (Fills<D, true>::two(dr))
+                            tc_commit(&ctl.empty[st]);
+                    }
+                    __syncwarp();
+                };
+                auto product = [&](int q) {
+                    const uint32_t s = (nj + (uint32_t)q) & 1u;
+                    const bool dr = draft && q == 0, two = Fills<D, true>::two(dr);
+                    const uint32_t f = base + Fills<D, true>::at(seg, q) + (two ? 1 : 0);
+                    const uint32_t st = __shfl_sync(0xffffffffu, f % kStages, 0);
+                    await(ctl, &ctl.full[st], f / kStages);
+                    if (dr || seg.valid(seg.t0 + q) < kTile)
+                        await(ctl, &ctl.fix[st], f / kStages);
+                    await(ctl, &ctl.p_full[s], (nj + (uint32_t)q) >> 1);
+                    if (dr) {  // only now: the last segment's has been read
+                        if (lane < 4)
+                            ctl.poison[lane] = ctl.poison_slot[st][lane];
+                        __syncwarp();
+                        if (issue)
+                            mbar_arrive(&ctl.poison_full);
+                    }
+                    tc_fence_after();
+                    const uint32_t su = __shfl_sync(0xffffffffu, s, 0);
+                    const uint32_t v = st * (uint32_t)(kSlotBytes / 16) + __shfl_sync(0xffffffffu, two ? 0u : (uint32_t)(kVoff / 16), 0);
+                    const uint32_t d = tmu, pb = su * (uint32_t)(N::kP / 16);
+                    const uint32_t acc = q >= 1;  // the segment's first product overwrites O^T
+                    if (issue) {
+                        if (dr) {
+#pragma unroll
+                            for (int kk = 0; kk < kTile / 16; ++kk)
+                                tc_mma_bf16(d, dV + v + 128u * kk, dP + pb + 128u * kk, idO, acc | (kk != 0));
+                        } else {
+#pragma unroll
+                            for (int kk = 0; kk < kTile / 32; ++kk)
+                                tc_mma_f8(d, dV8 + v + (uint32_t)(2 * D * kk), dP8 + pb + 128u * kk, idO8, acc | (kk != 0));
+                        }
+                        tc_commit(&ctl.o_full[s]);
+                        tc_commit(&ctl.empty[st]);
+                    }
+                    __syncwarp();
+                };
+                scores(0);
+                if (njobs > 1)
+                    scores(1);
+                for (int q = 0; q < njobs; ++q) {
+                    product(q);
+                    if (q + 2 < njobs)
+                        scores(q + 2);
+                }
+                nj += (uint32_t)njobs;
+                base += Fills<D, true>::at(seg, seg.n - 1) + (Fills<D, true>::two(draft && seg.n == 1) ? 2 : 1);
+            }
+            if (issue)
+                tc_commit(&ctl.done);
+            __syncwarp();
+        } else if (warp == 18) {
+            clear_values<D, true, kStages>(p, ctl, ring, lane);
+        } else {
+            // ---- scales: the bytes of four of a segment's tiles are on their way while one's are written (the next
+            // segment's only once this one's are written: its stages wait for this one's products) ----
+            uint32_t fill = 0, iseg = 0;
+            uint8_t sk[4][4], sv_[4][4];  // touched only when written: an operation on them would wait for the load
+            while (next_seg(ctl, iseg, seg)) {
+                if (seg.none())
+                    continue;
+                auto fetch = [&](uint8_t *k8, uint8_t *v8, int i) {
+                    const int key0 = seg.key0(seg.t0 + i) + lane;
+                    const long long at = ((long long)seg.b * p.L + key0) * p.H + seg.h;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int key = key0 + 32 * j;
+                        k8[j] = v8[j] = 127;
+                        if (key >= 0 && key < seg.keys) {
+                            k8[j] = __ldg(p.k_scale + at + 32 * j * p.H);
+                            v8[j] = __ldg(p.v_scale + at + 32 * j * p.H);
+                        }
+                    }
+                };
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (k < seg.n)
+                        fetch(sk[k], sv_[k], k);
+                for (int i0 = 0; i0 < seg.n; i0 += 4) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int i = i0 + k;
+                        if (i >= seg.n)
+                            break;
+                        const int ns = Fills<D, true>::two(seg.draft() && i == 0) ? 2 : 1;
+#pragma unroll 1
+                        for (int part = 0; part < ns; ++part, ++fill) {
+                            const int st = (int)(fill % kStages);
+                            if (fill >= (uint32_t)kStages)
+                                await(ctl, &ctl.empty[st], fill / kStages - 1);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                ctl.scale[st][lane + 32 * j] = (uint16_t)(sk[k][j] | (sv_[k][j] << 8));
+                            __syncwarp();
+                            if (lane == 0)
+                                mbar_arrive(&ctl.full[st]);
+                        }
+                        if (i + 4 < seg.n)
+                            fetch(sk[k], sv_[k], i + 4);
+                    }
+                }
+            }
+        }
+    } else {
+        regs_inc<kNarrowRegsSoftmax>();
+        const int wg = warp >> 2, wq = warp & 3, pt = tid & 127;
+        const int lo = 16 * wg, nrow = min(rows - lo, 16);  // this warpgroup's rows; none when nrow <= 0
+        const uint32_t lanes = (uint32_t)(wq * 32) << 16;
+        const uint32_t tS = tmem + lanes + 256 + lo, tO = tmem + lanes + lo;
+        float *nmu = &ctl.nmu[lo], *fac = &ctl.fac[lo], *mu = &ctl.mu[lo];
+        uint32_t nj = 0, npois = 0, nseg = 0, nconv = 0;
+        uint32_t base = 0;  // ring fills before this segment
+        uint32_t iseg = 0;
+        if (tid == 0)
+            hand_out_seg(ctl, 0);
+        bar_sync(1, kNarrowSoftmax);
+        while (get_seg(ctl.segs.cur[iseg & 1], seg)) {
+            ++iseg;
+            const bool draft = seg.draft(), none = seg.none();
+            const int njobs = none ? 0 : seg.n;
+            bool poison = false;
+            float cq = p.c;
+            if (!none) {
+                await(ctl, &ctl.qt_full[0], nseg++);
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&ctl.q_empty[0]);
+                if (!draft || seg.n > 1) {
+                    // Q -> two e4m3 terms; the last segment's products have read the codes
+                    constexpr int kPc = D / 8;
+                    const int end = rows * kPc;
+                    auto piece = [&](int e) {
+                        const int row = e / kPc, x = e % kPc;
+                        return *reinterpret_cast<const uint4 *>(smem + (x / 8) * kNarrowPanel + row * 128 + (((x & 7) ^ (row & 7)) * 16));
+                    };
+                    unsigned qm = 0;
+                    for (int e = tid; e < end; e += kNarrowSoftmax)
+                        qm = max(qm, finite_max(piece(e)));
+                    qm = __reduce_max_sync(0xffffffffu, qm);
+                    if (lane == 0)
+                        atomicMax(&ctl.qmax[nconv & 1u], qm);
+                    bar_sync(1, kNarrowSoftmax);
+                    const int e2 = code_exponent(ctl.qmax[nconv & 1u]);
+                    const float f = pow2i(-e2);
+                    cq = p.c * pow2i(e2);
+                    for (int e = tid; e < end; e += kNarrowSoftmax) {
+                        const int row = e / kPc, x = e % kPc;
+                        uint2 hi, l8;
+                        two_terms(piece(e), f, hi, l8);
+                        // 8 codes at byte 8 * x of a D-byte row, swizzled as TMA does for rows of D bytes
+                        const int ch = x >> 1, sw = D == 128 ? ch ^ (row & 7) : ch ^ ((row >> 1) & 3);
+                        unsigned char *at = qc + row * D + sw * 16 + (x & 1) * 8;
+                        *reinterpret_cast<uint2 *>(at) = hi;
+                        *reinterpret_cast<uint2 *>(at + kNarrowRows * D) = l8;
+                    }
+                    fence_async_shared();
+                    mbar_arrive(&ctl.q_full);
+                    bar_sync(1, kNarrowSoftmax);  // qmax has been read; it is used again after the next conversion's barriers
+                    if (tid == 0)
+                        ctl.qmax[nconv & 1u] = 0;
+                    ++nconv;
+                }
+            }
+            if (nrow <= 0) {
+                bar_sync(1, kNarrowSoftmax);
+                continue;
+            }
+            unsigned long long l2[8];  // this thread's sums of each row's weights
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                l2[k] = 0;
+            uint32_t vis = 0;  // this warpgroup's rows that see new token pt
+            if (draft) {
+                unsigned long long tok = 0;  // tokens that see it
+                const int32_t *par = p.parent ? p.parent + (long long)seg.b * p.T : nullptr;
+                bool bad = false;
+                if (par) {
+                    for (int k = lane; k < p.T; k += 32) {
+                        const int x = __ldg(&par[k]);
+                        bad |= k == 0 ? x != -1 : x < 0 || x >= k;
+                    }
+                    bad = __any_sync(0xffffffffu, bad);
+                }
+                if (bad) {
+                    poison = true;
+                    if (tid == 0 && p.status)
+                        atomicOr(p.status, SV_ATTN_BAD_TREE);
+                } else if (pt < p.T) {
+                    tok = par ? 1ull << pt : ~0ull << pt;
+                    if (par)
+                        for (int t = pt + 1; t < p.T; ++t)
+                            tok |= ((tok >> __ldg(&par[t])) & 1ull) << t;
+                }
+                int g = lo % p.G;
+                tok >>= lo / p.G;
+#pragma unroll 1
+                for (int k = 0; k < nrow; ++k) {
+                    vis |= (uint32_t)(tok & 1ull) << k;
+                    if (++g == p.G) {
+                        g = 0;
+                        tok >>= 1;
+                    }
+                }
+            }
+
+#pragma unroll 1
+            for (int q = 0; q < njobs; ++q, ++nj) {
+                const uint32_t s = nj & 1u, use = nj >> 1;  // buffers of S^T and P^T, and how often they were used
+                const bool dr = draft && q == 0;
+                await(ctl, &ctl.s_full[s], use);
+                tc_fence_after();
+                uint32_t x[16];
+                tmem_ld16_nowait(tS + 64 * s, x);
+                float f = p.c, ev = 0.0f, inv = 1.0f;
+                uint32_t see = 0xffffu;  // rows that see this thread's key
+                if (dr) {
+                    see = vis;
+                } else {
+                    const uint32_t fl = base + Fills<D, true>::at(seg, q), st = fl % kStages;
+                    await(ctl, &ctl.full[st], fl / kStages);  // complete: its product is; the stage stays until P is used
+                    const uint32_t sc = ctl.scale[st][pt];
+                    f = cq * __uint_as_float((sc & 255u) << 23);
+                    ev = (float)((int)(sc >> 8) - 127);
+                    inv = __uint_as_float((254u - min(sc >> 8, 254u)) << 23);
+                    if (pt >= seg.valid(seg.t0 + q))
+                        see = 0;
+                }
+                tmem_wait_ld();
+                // y = score * the key's factor + the exponent of the value's scale
+#pragma unroll
+                for (int k = 0; k < 16; k += 2)
+                    fma_pair(x[k], x[k + 1], f, f, ev, ev);
+                if (__any_sync(0xffffffffu, see != 0xffffu)) {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k)
+                        x[k] = (see >> k) & 1u ? x[k] : 0xff800000u;
+                }
+                if (q == 0) {  // first references: the best of four keys' scores
+                    if (lane == 0)
+#pragma unroll
+                        for (int k = 0; k < 16; k += 4)
+                            *reinterpret_cast<uint4 *>(&ctl.part[wg][wq][k]) = make_uint4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+                    bar_sync(2 + wg, 128);
+                    if (pt < 16) {
+                        const float a = fmaxf(fmaxf(ctl.part[wg][0][pt], ctl.part[wg][1][pt]), fmaxf(ctl.part[wg][2][pt], ctl.part[wg][3][pt]));
+                        // none of the four finite: start from 0
+                        const float m = a > -INFINITY && a < INFINITY ? a + kNarrowMargin : 0.0f;
+                        mu[pt] = m;
+                        nmu[pt] = kNarrowBase - m;
+                    }
+                    bar_sync(2 + wg, 128);
+                }
+                // z = y - mu + base, the logarithm of the weight
+                float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+                for (int k = 0; k < 16; k += 4) {
+                    const float4 n = *reinterpret_cast<const float4 *>(nmu + k);
+                    add_pair(x[k], x[k + 1], n.x, n.y);
+                    add_pair(x[k + 2], x[k + 3], n.z, n.w);
+                    m0 = fmaxf(m0, fmaxf(__uint_as_float(x[k]), __uint_as_float(x[k + 1])));
+                    m1 = fmaxf(m1, fmaxf(__uint_as_float(x[k + 2]), __uint_as_float(x[k + 3])));
+                }
+                if (any128(2 + wg, fmaxf(m0, m1) > kNarrowBase + kNarrowSlack)) {
+                    // some row has outgrown its reference: reduce the maxima, rescale
+                    int mine = 0;
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        const int r = __reduce_max_sync(0xffffffffu, ordered(__uint_as_float(x[k])));
+                        mine = lane == k ? r : mine;
+                    }
+                    if (lane < 16)
+                        ctl.part[wg][wq][lane] = unordered(mine);
+                    bar_sync(2 + wg, 128);
+                    if (pt < 16) {
+                        // the largest z, and how far the reference moves: up only
+                        const float z = fmax_nan(fmax_nan(ctl.part[wg][0][pt], ctl.part[wg][1][pt]), fmax_nan(ctl.part[wg][2][pt], ctl.part[wg][3][pt]));
+                        const float d = fmax_nan(z - kNarrowBase, 0.0f);
+                        mu[pt] += d;
+                        nmu[pt] = kNarrowBase - mu[pt];
+                        fac[pt] = -d;
+                    }
+                    bar_sync(2 + wg, 128);
+#pragma unroll
+                    for (int k = 0; k < 16; k += 4) {
+                        const float4 d = *reinterpret_cast<const float4 *>(fac + k);
+                        add_pair(x[k], x[k + 1], d.x, d.y);
+                        add_pair(x[k + 2], x[k + 3], d.z, d.w);
+                        l2[k / 2] = mul2(l2[k / 2], pack2(ex2(d.x), ex2(d.y)));
+                        l2[k / 2 + 1] = mul2(l2[k / 2 + 1], pack2(ex2(d.z), ex2(d.w)));
+                    }
+                    if (q > 0) {  // the last tile's product is complete before O^T is rescaled
+                        await(ctl, &ctl.o_full[(nj - 1) & 1u], (nj - 1) >> 1);
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c0 = 0; c0 < 192; c0 += 64) {
+                            uint32_t o[16];
+                            tmem_ld16_nowait(tO + c0, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int k = 0; k < 16; ++k)
+                                o[k] = __float_as_uint(__uint_as_float(o[k]) * ex2(fac[k]));
+                            tmem_st16(tO + c0, o);
+                        }
+                        tmem_wait_st();
+                    }
+                }
+                if (use > 0)  // the buffer's last product has read P
+                    await(ctl, &ctl.o_full[s], use - 1);
+                // w = 2^z, summed and rounded into P^T
+                const unsigned long long inv2 = pack2(inv, inv);
+                unsigned char *pslot = pw + s * N::kP;
+                uint32_t t[12];
+#pragma unroll
+                for (int k = 0; k < 16; k += 4) {
+                    float w[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        w[j] = ex2(__uint_as_float(x[k + j]));
+                    l2[k / 2] = fma2(pack2(w[0], w[1]), inv2, l2[k / 2]);
+                    l2[k / 2 + 1] = fma2(pack2(w[2], w[3]), inv2, l2[k / 2 + 1]);
+                    if (dr) {
+                        x[k / 2] = pack_bf16(w[0], w[1]);
+                        x[k / 2 + 1] = pack_bf16(w[2], w[3]);
+                    } else {
+                        three_terms(w, t[k / 4], t[4 + k / 4], t[8 + k / 4]);
+                    }
+                }
+                if (dr) {  // row pt of 128 bytes, swizzled
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        *reinterpret_cast<uint4 *>(pslot + pt * 128 + (((2 * wg + j) ^ (pt & 7)) * 16)) =
+                            make_uint4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+                    // their product writes the first part of O^T only
+#pragma unroll
+                    for (int k = 0; k < 16; ++k)
+                        x[k] = 0;
+                    tmem_st16(tO + 64, x);
+                    tmem_st16(tO + 128, x);
+                    tmem_wait_st();
+                } else {  // row pt of 64 bytes in each of the three
+#pragma unroll
+                    for (int part = 0; part < 3; ++part)
+                        *reinterpret_cast<uint4 *>(pslot + part * N::kTerm + pt * 64 + ((wg ^ ((pt >> 1) & 3)) * 16)) =
+                            make_uint4(t[4 * part], t[4 * part + 1], t[4 * part + 2], t[4 * part + 3]);
+                }
+                fence_async_shared();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&ctl.p_full[s]);
+            }
+            if (!none)
+                base += Fills<D, true>::at(seg, seg.n - 1) + (Fills<D, true>::two(draft && seg.n == 1) ? 2 : 1);
+
+            // ---- epilogue ----
+            if (!none)
+                await(ctl, &ctl.o_full[(nj - 1) & 1u], (nj - 1) >> 1);
+            float lv[16];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                unpack2(l2[k], lv[2 * k], lv[2 * k + 1]);
+            if (draft) {
+                await(ctl, &ctl.poison_full, npois++);
+                if ((ctl.poison[wq] >> lane) & 1u) {  // new token pt's values are not finite
+#pragma unroll
+                    for (int k = 0; k < 16; ++k)
+                        lv[k] = (vis >> k) & 1u ? nan_f() : lv[k];
+                }
+            }
+            const float sum = transpose_sum16(lv, lane);
+            if (lane < 16)
+                ctl.part[wg][wq][lane] = sum;
+            bar_sync(2 + wg, 128);
+            const bool direct = seg.whole();
+            float *slot = p.pieces + (size_t)(2 * blockIdx.x + (seg.first ? 0 : 1)) * p.rm * (D + 4);
+            if (pt < nrow) {
+                const int r = lo + pt;
+                const float l = poison || seg.bad ? nan_f() : (ctl.part[wg][0][pt] + ctl.part[wg][1][pt]) + (ctl.part[wg][2][pt] + ctl.part[wg][3][pt]);
+                const float R = none ? -INFINITY : mu[pt] - kNarrowBase;
+                float fa = 1.0f;
+                if (direct) {
+                    fa = l == 0.0f ? 0.0f : 1.0f / l;
+                    if (p.lse) {
+                        const int Rg = seg.row0 + r, tok = Rg / p.G;
+                        p.lse[(size_t)tok * p.Hq + seg.h * p.G + (Rg - tok * p.G)] = l == 0.0f ? -INFINITY : (R + log2f(l)) * 0.69314718055994531f;
+                    }
+                } else {
+                    *reinterpret_cast<float2 *>(slot + (size_t)p.rm * D + r * 2) = make_float2(R, l);
+                }
+                fac[pt] = l != l ? l : fa;  // NaN reaches every column
+            }
+            if (seg.bad && p.status && tid == 0)
+                atomicOr(p.status, SV_ATTN_BAD_LEN);
+            bar_sync(2 + wg, 128);
+            tc_fence_after();
+            if (D == 128 || wq < 2) {  // thread = channel
+                float o[16];
+                if (!none) {
+                    uint32_t y[48];
+#pragma unroll
+                    for (int part = 0; part < 3; ++part)
+                        tmem_ld16_nowait(tO + 64 * part, y + 16 * part);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 16; ++k)
+                        o[k] = fac[k] * ((__uint_as_float(y[k]) + __uint_as_float(y[16 + k])) + __uint_as_float(y[32 + k]));
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k)
+                        o[k] = seg.bad ? nan_f() : 0.0f;
+                }
+                const int d = 32 * wq + lane;
+                if (direct) {
+                    int tok = (seg.row0 + lo) / p.G, g = seg.row0 + lo - tok * p.G;
+                    __nv_bfloat16 *dst = p.out + ((size_t)tok * p.Hq + seg.h * p.G + g) * D + d;
+                    const int wrap = (p.Hq - p.G) * D;  // from the last row of a token to the next one's first
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        if (k < nrow)
+                            *dst = __float2bfloat16(o[k]);
+                        dst += D;
+                        if (++g == p.G) {
+                            g = 0;
+                            dst += wrap;
+                        }
+                    }
+                } else {
+                    float *dst = slot + (size_t)lo * D + d;
+#pragma unroll
+                    for (int k = 0; k < 16; ++k)
+                        if (k < nrow)
+                            dst[k * D] = o[k];
+                }
+            }
+            tc_fence_before();
+            if (tid == 0)
+                hand_out_seg(ctl, iseg);
+            bar_sync(1, kNarrowSoftmax);  // the segment is done with
+            tc_fence_after();
+        }
+    }
+    finish<kStages, 1>(p, ctl);
+    tc_fence_after();
+    if (warp == 17)
+        tmem_dealloc(tmem, kTmemCols);
+}
+
+} // namespace

@@ -75,7 +75,7 @@ typedef enum { SV_KV_BF16 = 0, SV_KV_E4M3 = 1 } sv_kv_format;
  * head_dim not a multiple of 16 in 16 .. 256, a needed pointer NULL, rows or
  * cache not 16-byte aligned; SV_ERR_DTYPE: unknown format; SV_ERR_TOO_LARGE:
  * more than 65535 sequences, T > 1024 or byte offsets that would pass 2^62.
- * One kernel launch.
+ * One kernel launch, two when out_len is cache_len.
  */
 enum { SV_KV_BAD_PATH = 4, SV_KV_NONFINITE = 8 };
 

@@ -11,6 +11,7 @@ Python or CPU fallback, and importing a missing library raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import struct
@@ -224,7 +225,7 @@ def spec_verify_kv_read(cache, scale, cache_len, start, out, status, planes, B, 
                                       head_dim, stream)
 
 
-# sv_attention_args: 15 pointers, the softmax status, workspace and size, 4 strides, 8 sizes, the scale
+# sv_attention_args: 17 pointers, the workspace's size, 4 strides, 8 sizes, the softmax scale
 _ATTENTION_ARGS = struct.Struct("=17Q1q4q8qd")
 
 
@@ -458,31 +459,38 @@ def kv_commit(scratch, cache, cache_len, num_accepted, status=None, stream=None)
 def _kv_format(cache, scale, what):
     """The sv_kv_format of a cache tensor, its scale tensor checked: uint8, one byte a (row, head)."""
     import torch
-    if cache.dtype == torch.bfloat16:
+    if cache.dtype is torch.bfloat16:
         if scale is not None:
             raise ValueError(f"a bf16 {what} has no scales")
         return SV_KV_BF16
-    if cache.dtype != torch.float8_e4m3fn:
+    if cache.dtype is not torch.float8_e4m3fn:
         raise ValueError(f"{what} must be bfloat16 or float8_e4m3fn, got {cache.dtype}")
-    if scale is None or scale.dtype != torch.uint8 or scale.shape != cache.shape[:-1] or not scale.is_contiguous() \
-            or scale.device != cache.device:
+    if scale is None or scale.dtype is not torch.uint8 or scale.shape != cache.shape[:-1] \
+            or not scale.is_contiguous() or scale.get_device() != cache.get_device():
         raise ValueError(f"an e4m3 {what} needs contiguous uint8 scales of shape {tuple(cache.shape[:-1])}")
     return SV_KV_E4M3
 
 
-def _int32(name, t, shape, device):
+def _int32(name, t, shape, index):
+    """t is contiguous int32 of that shape on CUDA device ``index``."""
     import torch
-    if t.dtype != torch.int32 or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)} on {device}")
+    if t.dtype is not torch.int32 or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)} on cuda:{index}")
 
 
-def _on(device, call, *args):
-    """call(*args) with ``device`` current."""
+def _on(index, call, *args):
+    """call(*args) with CUDA device ``index`` current."""
     import torch
-    if torch.cuda.current_device() == device.index:
+    if torch.cuda.current_device() == index:
         return call(*args)
-    with torch.cuda.device(device):
+    with torch.cuda.device(index):
         return call(*args)
+
+
+def _raw_stream(index, stream):
+    """The cudaStream_t of ``stream``, or of the device's current one."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
 def kv_commit_path(rows, cache, cache_len, num_accepted, path=None, lead=0, scale=None, out_len=None, status=None,
@@ -500,26 +508,30 @@ def kv_commit_path(rows, cache, cache_len, num_accepted, path=None, lead=0, scal
     that collects SV_KV_* bits.  Enqueues on the current torch stream (or
     ``stream``) and does not synchronise."""
     import torch
-    if rows.dim() != 5 or cache.dim() != 5 or rows.shape[:2] != cache.shape[:2] or rows.shape[3:] != cache.shape[3:]:
+    if rows.dim() != 5 or cache.dim() != 5:
+        raise ValueError(f"rows {tuple(rows.shape)} and cache {tuple(cache.shape)} must have five dimensions")
+    P, B, T, H, D = rows.shape
+    L = cache.shape[2]
+    dev = cache.get_device()
+    if cache.shape != (P, B, L, H, D):
         raise ValueError(f"rows {tuple(rows.shape)} and cache {tuple(cache.shape)} do not match")
-    if rows.dtype != torch.bfloat16 or not rows.is_contiguous() or not cache.is_contiguous() or not cache.is_cuda \
-            or rows.device != cache.device:
+    if rows.dtype is not torch.bfloat16 or not rows.is_contiguous() or not cache.is_contiguous() or dev < 0 \
+            or rows.get_device() != dev:
         raise ValueError("rows must be bfloat16, rows and cache contiguous on one CUDA device")
     fmt = _kv_format(cache, scale, "cache")
-    P, B, T, H, D = rows.shape
-    dev = cache.device
     if out_len is None:
         out_len = cache_len
+    else:
+        _int32("out_len", out_len, (B,), dev)
     _int32("cache_len", cache_len, (B,), dev)
-    _int32("out_len", out_len, (B,), dev)
     _int32("num_accepted", num_accepted, (B,), dev)
     if path is not None:
         _int32("path", path, (B, T), dev)
     if status is not None:
         _int32("status", status, (1,), dev)
-    s = stream if stream is not None else torch.cuda.current_stream(dev)
-    st = _on(dev, spec_verify_kv_commit_path, _ptr(rows), _ptr(cache), _ptr(scale), _ptr(cache_len), _ptr(out_len),
-             _ptr(num_accepted), _ptr(path), _ptr(status), P, B, T, lead, cache.shape[2], H, D, fmt, s.cuda_stream)
+    st = _on(dev, spec_verify_kv_commit_path, rows.data_ptr(), cache.data_ptr(), _ptr(scale), cache_len.data_ptr(),
+             out_len.data_ptr(), num_accepted.data_ptr(), _ptr(path), _ptr(status), P, B, T, lead, L, H, D, fmt,
+             _raw_stream(dev, stream))
     if st != SV_OK:
         raise SpecVerifyError(st, "spec_verify_kv_commit_path")
     return out_len
@@ -533,41 +545,49 @@ def kv_read(cache, scale, cache_len, start=None, rows=None, out=None, status=Non
     past a sequence's last one are left as they were).  Enqueues on the
     current torch stream (or ``stream``) and does not synchronise."""
     import torch
-    if cache.dim() != 5 or not cache.is_contiguous() or not cache.is_cuda or cache.dtype != torch.float8_e4m3fn:
+    dev = cache.get_device()
+    if cache.dim() != 5 or not cache.is_contiguous() or dev < 0 or cache.dtype is not torch.float8_e4m3fn:
         raise ValueError("cache must be a contiguous float8_e4m3fn CUDA tensor [P, B, max_len, heads, head_dim]")
     _kv_format(cache, scale, "cache")
     P, B, L, H, D = cache.shape
-    dev = cache.device
-    s = stream if stream is not None else torch.cuda.current_stream(dev)
     if out is None:
-        with torch.cuda.stream(s):
-            out = torch.zeros((P, B, L if rows is None else rows, H, D), dtype=torch.bfloat16, device=dev)
+        with torch.cuda.stream(stream):
+            out = torch.zeros((P, B, L if rows is None else rows, H, D), dtype=torch.bfloat16, device=cache.device)
     n = out.shape[2] if out.dim() == 5 else -1
-    if out.shape != (P, B, n, H, D) or (rows is not None and n != rows) or out.dtype != torch.bfloat16 \
-            or not out.is_contiguous() or out.device != dev:
+    if out.shape != (P, B, n, H, D) or (rows is not None and n != rows) or out.dtype is not torch.bfloat16 \
+            or not out.is_contiguous() or out.get_device() != dev:
         raise ValueError("out must be contiguous bfloat16 [P, B, rows, heads, head_dim] on the cache's device")
     _int32("cache_len", cache_len, (B,), dev)
     if start is not None:
         _int32("start", start, (B,), dev)
     if status is not None:
         _int32("status", status, (1,), dev)
-    st = _on(dev, spec_verify_kv_read, _ptr(cache), _ptr(scale), _ptr(cache_len), _ptr(start), _ptr(out), _ptr(status),
-             P, B, n, L, H, D, s.cuda_stream)
+    st = _on(dev, spec_verify_kv_read, cache.data_ptr(), scale.data_ptr(), cache_len.data_ptr(), _ptr(start),
+             out.data_ptr(), _ptr(status), P, B, n, L, H, D, _raw_stream(dev, stream))
     if st != SV_OK:
         raise SpecVerifyError(st, "spec_verify_kv_read")
     return out
 
 
-def _tokens(name, t, shape, device):
+def _tokens(name, t, shape, index):
     """Strides (between sequences, between tokens) of a bf16 [B, T, heads, head_dim] tensor whose last two
     dimensions are contiguous."""
     import torch
-    if t.dtype != torch.bfloat16 or t.shape != shape or t.device != device:
-        raise ValueError(f"{name} must be bfloat16 {tuple(shape)} on {device}, got {t.dtype} {tuple(t.shape)}")
+    if t.dtype is not torch.bfloat16 or t.shape != shape or t.get_device() != index:
+        raise ValueError(f"{name} must be bfloat16 {tuple(shape)} on cuda:{index}, got {t.dtype} {tuple(t.shape)}")
     sb, st, sh, sd = t.stride()
     if (sd != 1 and shape[3] > 1) or (sh != shape[3] and shape[2] > 1):
         raise ValueError(f"{name}'s heads and head_dim must be contiguous")
     return sb if shape[0] > 1 else 0, st if shape[1] > 1 else 0
+
+
+@functools.lru_cache(maxsize=1024)
+def _attention_bytes(B, T, Hq, H, D, L, Lp, fmt):
+    """Workspace of an attention call: arithmetic on its sizes."""
+    st, n = spec_verify_attention_workspace(_ATTENTION_ARGS.pack(*(0,) * 22, B, T, Hq, H, D, L, Lp, fmt, 1.0))
+    if st != SV_OK:
+        raise SpecVerifyError(st, "spec_verify_attention")
+    return n
 
 
 def verify_attention(q, k_cache, v_cache, cache_len, k_new=None, v_new=None, parent=None, k_prefix=None,
@@ -590,74 +610,69 @@ def verify_attention(q, k_cache, v_cache, cache_len, k_new=None, v_new=None, par
     bits.  Returns out [B, T, heads_q, D] bf16; enqueues on the current torch
     stream (or ``stream``) and does not synchronise."""
     import torch
-    if q.dim() != 4 or k_cache.dim() != 4 or not q.is_cuda:
+    dev = q.get_device()
+    if q.dim() != 4 or k_cache.dim() != 4 or dev < 0:
         raise ValueError("q must be a CUDA tensor [B, T, heads_q, head_dim], the caches [B, max_len, heads_kv, head_dim]")
     B, T, Hq, D = q.shape
-    L, H = k_cache.shape[1:3]
-    dev = q.device
+    _, L, H, _ = k_cache.shape
     qb, qt = _tokens("q", q, q.shape, dev)
-    if k_cache.shape != (B, L, H, D) or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype \
-            or k_cache.device != dev or v_cache.device != dev or not k_cache.is_contiguous() \
+    if k_cache.shape != (B, L, H, D) or v_cache.shape != (B, L, H, D) or v_cache.dtype is not k_cache.dtype \
+            or k_cache.get_device() != dev or v_cache.get_device() != dev or not k_cache.is_contiguous() \
             or not v_cache.is_contiguous():
         raise ValueError(f"k_cache and v_cache must be contiguous [{B}, max_len, heads_kv, {D}] of one type")
     fmt = _kv_format(k_cache, k_scale, "k_cache")
     _kv_format(v_cache, v_scale, "v_cache")
     _int32("cache_len", cache_len, (B,), dev)
-    nb = nt = 0
     if (k_new is None) != (v_new is None) or (k_prefix is None) != (v_prefix is None):
         raise ValueError("keys and values come together")
+    nb = nt = kn = vn = par = kp = vp = Lp = 0
     if k_new is not None:
         nb, nt = _tokens("k_new", k_new, (B, T, H, D), dev)
         if _tokens("v_new", v_new, (B, T, H, D), dev) != (nb, nt):
             raise ValueError("k_new and v_new must have the same strides")
+        kn, vn = k_new.data_ptr(), v_new.data_ptr()
         if parent is not None:
             _int32("parent", parent, (B, T), dev)
+            par = parent.data_ptr()
     elif parent is not None:
         raise ValueError("parent goes with k_new and v_new")
-    Lp = 0
     if k_prefix is not None:
         Lp = k_prefix.shape[0]
         for name, t, ts in (("k_prefix", k_prefix, k_prefix_scale), ("v_prefix", v_prefix, v_prefix_scale)):
-            if t.shape != (Lp, H, D) or t.dtype != k_cache.dtype or t.device != dev or not t.is_contiguous():
+            if t.shape != (Lp, H, D) or t.dtype is not k_cache.dtype or t.get_device() != dev or not t.is_contiguous():
                 raise ValueError(f"{name} must be contiguous [prefix_len, {H}, {D}] of the cache's type")
             _kv_format(t, ts, name)
-    if out is not None and (out.shape != q.shape or out.dtype != torch.bfloat16 or not out.is_contiguous()
-                            or out.device != dev):
+        kp, vp = k_prefix.data_ptr(), v_prefix.data_ptr()
+    elif k_prefix_scale is not None or v_prefix_scale is not None:
+        raise ValueError("prefix scales go with a prefix")
+    if out is not None and (out.shape != q.shape or out.dtype is not torch.bfloat16 or not out.is_contiguous()
+                            or out.get_device() != dev):
         raise ValueError("out must be contiguous bfloat16 of q's shape")
-    if lse is not None and (lse.shape != (B, T, Hq) or lse.dtype != torch.float32 or not lse.is_contiguous()
-                            or lse.device != dev):
+    if lse is not None and (lse.shape != (B, T, Hq) or lse.dtype is not torch.float32 or not lse.is_contiguous()
+                            or lse.get_device() != dev):
         raise ValueError("lse must be contiguous float32 [B, T, heads_q]")
     if status is not None:
         _int32("status", status, (1,), dev)
-    if scale is None:
-        scale = D ** -0.5
-    own = stream is None
-    s = torch.cuda.current_stream(dev) if own else stream
-
-    def p(t):
-        return 0 if t is None else t.data_ptr()
-
-    def packed(ws, nbytes):
-        return _ATTENTION_ARGS.pack(
-            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), p(k_scale), p(v_scale), cache_len.data_ptr(),
-            p(k_prefix), p(v_prefix), p(k_prefix_scale), p(v_prefix_scale), p(k_new), p(v_new), p(parent), p(out),
-            p(lse), p(status), ws, nbytes, qb, qt, nb, nt, B, T, Hq, H, D, L, Lp, fmt, scale)
-
-    st, nbytes = spec_verify_attention_workspace(packed(0, 0))
-    if st != SV_OK:
-        raise SpecVerifyError(st, "spec_verify_attention")
+    nbytes = _attention_bytes(B, T, Hq, H, D, L, Lp, fmt)
     # the workspace comes from the caching allocator, for this call alone: calls on
     # other streams and captured graphs each have their own
-    if own:
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    if stream is None:
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
         if out is None:
-            out = torch.empty((B, T, Hq, D), dtype=torch.bfloat16, device=dev)
+            out = torch.empty((B, T, Hq, D), dtype=torch.bfloat16, device=q.device)
     else:
-        with torch.cuda.stream(s):
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        with torch.cuda.stream(stream):
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
             if out is None:
-                out = torch.empty((B, T, Hq, D), dtype=torch.bfloat16, device=dev)
-    st = _on(dev, spec_verify_attention, packed(ws.data_ptr(), nbytes), s.cuda_stream)
+                out = torch.empty((B, T, Hq, D), dtype=torch.bfloat16, device=q.device)
+    args = _ATTENTION_ARGS.pack(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), 0 if k_scale is None else k_scale.data_ptr(),
+        0 if v_scale is None else v_scale.data_ptr(), cache_len.data_ptr(), kp, vp,
+        0 if k_prefix_scale is None else k_prefix_scale.data_ptr(),
+        0 if v_prefix_scale is None else v_prefix_scale.data_ptr(), kn, vn, par, out.data_ptr(),
+        0 if lse is None else lse.data_ptr(), 0 if status is None else status.data_ptr(), ws.data_ptr(), nbytes, qb, qt,
+        nb, nt, B, T, Hq, H, D, L, Lp, fmt, D ** -0.5 if scale is None else scale)
+    st = _on(dev, spec_verify_attention, args, _raw_stream(dev, stream))
     if st != SV_OK:
         raise SpecVerifyError(st, "spec_verify_attention")
     return out

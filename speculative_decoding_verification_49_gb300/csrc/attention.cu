@@ -82,7 +82,6 @@ constexpr int kThreads = 384;          // warp 11 idles: registers are moved by 
 // other 128 keep 72: the same 64512 in all
 constexpr int kRegsStart = 168, kRegsSoftmax = 216, kRegsOther = 72;
 static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * kRegsStart, "the split is covered by what the launch holds");
-constexpr int kSegCost = 1;           // what a segment costs beside its tiles, in tiles
 constexpr int kMaxCtas = 160;         // of the grid; the workspace counts on it
 constexpr uint32_t kTmemCols = 512;
 constexpr uint64_t kWaitNs = 2000000000ull;
@@ -111,6 +110,7 @@ struct AttnParams {
     long long q_sb, q_st;
     int B, T, Hq, H, G, L, Lp;
     int has_new, max_len;
+    int seg_cost;           // what a segment counts beside its tiles, in tiles
     int tma_q;              // a sequence's rows fit one slot: their queries come by TMA
     int nbp, ntp, UP;       // prefix: row blocks and tiles a head, units in all
     int nbs;                // row blocks of a sequence's rows
@@ -235,7 +235,7 @@ struct Seg {
 };
 
 // Walks the segments of a CTA's stretch; every role walks the same ones.  A
-// segment takes kSegCost units ahead of its tiles' units; a stretch that holds
+// segment takes seg_cost units ahead of its tiles' units; a stretch that holds
 // only such units of it has no part in it.
 struct Walk {
     int u, u0, u1, b, ub, raw, raw_next;
@@ -250,13 +250,13 @@ struct Walk {
         raw_next = raw_len(p, b + 1);
     }
 
-    // Tiles of [u, u1) in the segment of units us .. us + kSegCost + nt - 1; moves u to its end.
-    __device__ void cut(Seg &s, int us)
+    // Tiles of [u, u1) in the segment of units us .. us + cost + nt - 1; moves u to its end.
+    __device__ void cut(Seg &s, int us, int cost)
     {
-        const int e = min(u1, us + kSegCost + s.nt);
+        const int e = min(u1, us + cost + s.nt);
         s.first = u0 >= us;
-        s.t0 = max(u - us - kSegCost, 0);
-        s.n = max(e - us - kSegCost, 0) - s.t0;
+        s.t0 = max(u - us - cost, 0);
+        s.n = max(e - us - cost, 0) - s.t0;
         u = e;
     }
 
@@ -264,7 +264,7 @@ struct Walk {
     {
         while (u < u1) {
             if (u < p.UP) {
-                const int per = p.ntp + kSegCost;
+                const int per = p.ntp + p.seg_cost;
                 s.id = u / per;
                 s.nt = p.ntp;
                 s.prefix = true;
@@ -276,11 +276,11 @@ struct Walk {
                 s.nrows = min(2 * kTile, p.B * p.T * p.G - s.row0);
                 s.keys = p.Lp;
                 s.hn = 0;
-                cut(s, s.id * per);
+                cut(s, s.id * per, p.seg_cost);
             } else {
                 const Len len = clean_len(p, raw);
                 s.nt = tiles_of(p, len.n);
-                const int per = s.nt + kSegCost, rel = (u - ub) / per;
+                const int per = s.nt + p.seg_cost, rel = (u - ub) / per;
                 s.prefix = false;
                 s.tq = p.tma_q;
                 s.bad = len.bad;
@@ -292,7 +292,7 @@ struct Walk {
                 s.keys = len.n;
                 s.hn = p.has_new;
                 s.id = (b * p.H + s.h) * p.nbs + s.rb;
-                cut(s, ub + rel * per);
+                cut(s, ub + rel * per, p.seg_cost);
                 if (u == ub + p.H * p.nbs * per) {
                     ub = u;
                     ++b;
@@ -485,7 +485,7 @@ template <int kThr, class Ct> __device__ __forceinline__ void find_stretch(const
     const int bs = min(p.B, tid * chunk), be = min(p.B, bs + chunk);
     int mine = 0;
     for (int b = bs; b < be; ++b)
-        mine += (kSegCost + tiles_of(p, clean_len(p, raw_len(p, b)).n));
+        mine += (p.seg_cost + tiles_of(p, clean_len(p, raw_len(p, b)).n));
     int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -516,7 +516,7 @@ template <int kThr, class Ct> __device__ __forceinline__ void find_stretch(const
         const bool holds = target >= ub && target < ub + per * mine;
         if (holds || blockIdx.x == 0)
             for (int b = bs; b < be; ++b) {
-                const int next = ub + per * (kSegCost + tiles_of(p, clean_len(p, raw_len(p, b)).n));
+                const int next = ub + per * (p.seg_cost + tiles_of(p, clean_len(p, raw_len(p, b)).n));
                 if (target >= ub && target < next) {
                     ctl.start_b = b;
                     ctl.start_ub = ub;
@@ -1388,11 +1388,11 @@ template <int D, int W, bool PREFIX> __global__ void __launch_bounds__(256) sv_a
         R = tok * p.G + (hq - h * p.G);
         local = R - b * p.T * p.G;
         const int ub = __ldg(&p.seg_start[b]), ue = __ldg(&p.seg_start[b + 1]);
-        nt = (ue - ub) / (p.H * p.nbs) - kSegCost;
+        nt = (ue - ub) / (p.H * p.nbs) - p.seg_cost;
         const int rb = local / (2 * kTile);
         id_s = (b * p.H + h) * p.nbs + rb;
-        us = ub + (h * p.nbs + rb) * (nt + kSegCost);
-        ut = us + kSegCost;  // its first tile's unit
+        us = ub + (h * p.nbs + rb) * (nt + p.seg_cost);
+        ut = us + p.seg_cost;  // its first tile's unit
         rb_row = local % (2 * kTile);
     } else {
         const int4 cut = __ldg(&p.cuts[2 * blockIdx.x]);
@@ -1403,7 +1403,7 @@ template <int D, int W, bool PREFIX> __global__ void __launch_bounds__(256) sv_a
         if (cut.x < 0 || rb_row >= cut.y || owner(ut, U, C) != (int)blockIdx.x - 1)
             return;
         h = __ldg(&p.cuts[2 * blockIdx.x + 1]).x;
-        us = ut - kSegCost;
+        us = ut - p.seg_cost;
         R = cut.x + rb_row;
         const int tok = R / p.G;
         row = (long long)tok * p.Hq + h * p.G + (R - tok * p.G);
@@ -1412,9 +1412,9 @@ template <int D, int W, bool PREFIX> __global__ void __launch_bounds__(256) sv_a
     int id_p = 0, up = 0, p0 = 0, p1 = -1;
     if constexpr (PREFIX) {
         id_p = h * p.nbp + R / (2 * kTile);
-        up = id_p * (p.ntp + kSegCost);
-        p0 = owner(up + kSegCost, U, C);
-        p1 = owner(up + kSegCost + p.ntp - 1, U, C);
+        up = id_p * (p.ntp + p.seg_cost);
+        p0 = owner(up + p.seg_cost, U, C);
+        p1 = owner(up + p.seg_cost + p.ntp - 1, U, C);
     }
     const int np = p1 - p0 + 1, n = np + (s1 - s0 + 1);
     // part i: its row of O, and (R, l)
@@ -1556,7 +1556,7 @@ sv_status check(const sv_attention_args *a)
 
 // Sizes of a call, false when they pass the 32-bit counts of the kernels.
 struct Plan {
-    int G, nbp, ntp, nbs, rp, rs, rm;
+    int G, nbp, ntp, nbs, rp, rs, rm, seg_cost;
     int64_t UP, most;  // prefix units, units at full lengths
     int64_t off_cut, off_wp, off_ws, off_pc, bytes;
 };
@@ -1567,12 +1567,16 @@ bool plan(const sv_attention_args &a, Plan &w)
     if (a.heads_q > big / 4 || a.max_len > big - 256 || a.prefix_len > big - 256 || a.B > big / a.T / a.heads_q)
         return false;
     w.G = (int)(a.heads_q / a.heads_kv);
+    // A segment's start and end (queries, epilogue) against a tile, so that short segments and long ones fill the
+    // stretches alike.  Measured: 256 chains of 8 over up to 2048 keys 124, 116, 114 us with 1, 2, 3; of 6 over 4096 e4m3
+    // keys 282, 261, 253, 248 us with 1, 3, 4, 6; with a prefix (long segments, all alike) 1 is best, 108 against 111 us.
+    w.seg_cost = a.format == SV_KV_E4M3 && a.prefix_len == 0 && a.T * w.G <= kNarrowMost ? 6 : a.prefix_len == 0 ? 3 : 1;
     const int64_t rows = a.B * a.T * w.G, seq_rows = a.T * w.G;
     w.ntp = (int)((a.prefix_len + kTile - 1) / kTile);
     w.nbp = (int)((rows + 2 * kTile - 1) / (2 * kTile));
     w.nbs = (int)((seq_rows + 2 * kTile - 1) / (2 * kTile));
-    w.UP = a.prefix_len > 0 ? a.heads_kv * w.nbp * (w.ntp + kSegCost) : 0;  // below 2^31 * 2^24
-    const int64_t tiles = (a.max_len + kTile - 1) / kTile + 1 + kSegCost;
+    w.UP = a.prefix_len > 0 ? a.heads_kv * w.nbp * (w.ntp + w.seg_cost) : 0;  // below 2^31 * 2^24
+    const int64_t tiles = (a.max_len + kTile - 1) / kTile + 1 + w.seg_cost;
     if (w.UP > big / 2 || a.heads_kv * w.nbs > big || a.B * a.heads_kv * w.nbs > big || tiles > big / 2 / (a.B * a.heads_kv * w.nbs + 1))
         return false;
     w.most = w.UP + a.B * a.heads_kv * w.nbs * tiles;
@@ -1602,10 +1606,11 @@ bool al16(const void *p)
 
 template <int D> cudaError_t set_attr()
 {
-    const void *kernels[3] = {(const void *)sv_attention_kernel<D, false>, (const void *)sv_attention_kernel<D, true>,
-                              (const void *)sv_attention_narrow_kernel<D>};
-    const size_t bytes[3] = {smem_bytes<D, false>(), smem_bytes<D, true>(), narrow_smem<D>()};
-    for (int i = 0; i < 3; ++i) {
+    const void *kernels[5] = {(const void *)sv_attention_kernel<D, false>, (const void *)sv_attention_kernel<D, true>,
+                              (const void *)sv_attention_narrow_kernel<D, 8>, (const void *)sv_attention_narrow_kernel<D, 16>,
+                              (const void *)sv_attention_narrow_kernel<D, 24>};
+    const size_t bytes[5] = {smem_bytes<D, false>(), smem_bytes<D, true>(), narrow_smem<D>(), narrow_smem<D>(), narrow_smem<D>()};
+    for (int i = 0; i < 5; ++i) {
         const cudaError_t e = cudaFuncSetAttribute(kernels[i], cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes[i]);
         if (e != cudaSuccess)
             return e;
@@ -1647,10 +1652,13 @@ template <int D, bool E4> sv_status launch(const Maps &maps, const AttnParams &p
     cfg.numAttrs = 1;
     cudaError_t e;
     // 8-bit caches, few rows and no prefix: the products turned around (attention_narrow.cuh)
-    if (E4 && p.UP == 0 && p.T * p.G <= kNarrowRows) {
+    const int rows = p.T * p.G;
+    if (E4 && p.UP == 0 && rows <= kNarrowMost) {
         cfg.blockDim = dim3(kNarrowThreads);
         cfg.dynamicSmemBytes = narrow_smem<D>();
-        e = cudaLaunchKernelEx(&cfg, sv_attention_narrow_kernel<D>, maps, p);
+        e = rows <= 16   ? cudaLaunchKernelEx(&cfg, sv_attention_narrow_kernel<D, 8>, maps, p)
+            : rows <= 32 ? cudaLaunchKernelEx(&cfg, sv_attention_narrow_kernel<D, 16>, maps, p)
+                         : cudaLaunchKernelEx(&cfg, sv_attention_narrow_kernel<D, 24>, maps, p);
     } else {
         cfg.blockDim = dim3(kThreads);
         cfg.dynamicSmemBytes = smem_bytes<D, E4>();
@@ -1658,12 +1666,12 @@ template <int D, bool E4> sv_status launch(const Maps &maps, const AttnParams &p
     }
     if (e == cudaSuccess) {
         // few rows: a CTA joins one row, its parts dealt to the warps
-        const long long rows = (long long)p.B * p.T * p.Hq;
+        const long long all = (long long)p.B * p.T * p.Hq;
         cfg.blockDim = dim3(256);
         cfg.dynamicSmemBytes = 0;
         if (p.UP > 0) {
-            const bool wide = rows <= 1024;
-            cfg.gridDim = dim3((unsigned)(wide ? rows : (rows + 7) / 8));
+            const bool wide = all <= 1024;
+            cfg.gridDim = dim3((unsigned)(wide ? all : (all + 7) / 8));
             e = wide ? cudaLaunchKernelEx(&cfg, sv_attention_join_kernel<D, 8, true>, p, C)
                      : cudaLaunchKernelEx(&cfg, sv_attention_join_kernel<D, 1, true>, p, C);
         } else {
@@ -1746,6 +1754,7 @@ extern "C" sv_status spec_verify_attention(const sv_attention_args *args, void *
         map(&maps.kn, a.k_new, false, a.B, a.T, sb, sn);
         map(&maps.vn, a.v_new, false, a.B, a.T, sb, sn);
     }
+    p.seg_cost = w.seg_cost;
     p.tma_q = a.T * w.G <= kTile;
     if (p.tma_q) {  // box: one token range's rows of one head, 64 wide
         const int64_t st_ = a.T > 1 ? a.q_stride_t : qrow, sb_ = a.B > 1 ? a.q_stride_b : a.T * st_;

@@ -1,5 +1,5 @@
 // attention_narrow.cuh -- the attention of attention.cu over e4m3 caches for
-// sequences of at most 64 (token, query head) rows a key/value head and no shared
+// sequences of at most 48 (token, query head) rows a key/value head and no shared
 // prefix: single tokens and chains of a few drafts.
 //
 // With 8-bit keys and values a tile's HBM time halves, and the products of
@@ -22,12 +22,14 @@
 // is 128 B a cycle): 32 KB by TMA, 48 + 40 read by the products, 24 of P: 1150 cycles
 // against 1400 of HBM time.
 //
-// Four warpgroups do the softmax, each of 16 rows (those behind the last row idle), on
-// every tile: few enough values for a thread that none is spilled.  S^T and P^T are double, so
-// that the products of one tile run beside the softmax of the next; O^T is single.
-//   warps 0-15   warpgroup g: rows 16 g ..; thread = key, then channel
+// Four warpgroups do the softmax: two slots, which take alternate tiles (what bounds a warpgroup is
+// its chain of dependent instructions for a tile), each with its own S^T, P^T and O^T, and in each two
+// groups of RW = 8, 16 or 24 rows, independent of each other.  24 rows a thread is what
+// the registers hold: beside this much shared memory the L1 is small, and a spilled value pays
+// memory latency.
+//   warps 0-15   warpgroup w: rows RW (w >> 1) .., slot w & 1; thread = key, then channel
 //   warps 16-19  producer, MMA issuer, clearing warp, as in attention.cu; the keys' scales into shared memory
-// TMEM: O^T at column 0 (three parts of 64), S^T at 256 and 320.
+// TMEM: O^T of the slots at columns 0 and 192 (three parts of 64), S^T at 384 and 448.
 // Walk, ring, stretches, clearing and joining are attention.cu's.
 #pragma once
 
@@ -35,7 +37,9 @@ namespace {
 
 constexpr int kNarrowRows = 64, kNarrowStages = 4;
 constexpr int kNarrowPanel = kNarrowRows * 128;  // 64 rows of 128 bytes of Q
+constexpr int kNarrowMost = 48;                  // rows that the kernel takes
 constexpr int kNarrowSoftmax = 512, kNarrowThreads = 640;
+constexpr int kNarrowAux = kNarrowSoftmax / 32;  // the first of the other warps
 // 640 threads start with 96 registers; the 512 softmax threads take 104, the others keep 64
 constexpr int kNarrowRegsStart = 96, kNarrowRegsSoftmax = 104, kNarrowRegsOther = 64;
 static_assert(kNarrowSoftmax * kNarrowRegsSoftmax + (kNarrowThreads - kNarrowSoftmax) * kNarrowRegsOther <=
@@ -66,11 +70,11 @@ struct NarrowCtl {
     int abort;
     int start_b, start_ub;
     SegRing segs;
-    // per row
-    alignas(16) float nmu[kNarrowRows];      // base - mu
-    alignas(16) float fac[kNarrowRows];      // the last move of the reference; at the end the row's factor
-    alignas(16) float part[4][4][16];        // per warpgroup and warp: sampled scores, maxima, sums of its rows
-    float mu[kNarrowRows];
+    // per slot and row
+    alignas(16) float nmu[2][kNarrowRows];   // base - mu
+    alignas(16) float fac[2][kNarrowRows];   // the last move of the reference; at the end the slots' factors
+    alignas(16) float part[4][4][32];        // per warpgroup and warp: sampled scores, maxima, sums of its rows
+    float mu[2][kNarrowRows], l[2][kNarrowRows];
     uint16_t scale[kNarrowStages][kTile];    // of a stage's keys: K's scale byte, V's in the upper half
 };
 
@@ -107,14 +111,16 @@ __device__ __forceinline__ bool any128(int id, bool x)
     return r != 0;
 }
 
-// Sums 16 values over the warp: lanes i and i + 16 return the total of v[i].
-__device__ __forceinline__ float transpose_sum16(float *v, int lane)
+// Sums 8 values over the warp: every lane returns the total of v[lane & 7].
+__device__ __forceinline__ float transpose_sum8(float *v, int lane)
 {
 #pragma unroll
-    for (int k = 0; k < 16; ++k)
-        v[k] += __shfl_xor_sync(0xffffffffu, v[k], 16);
+    for (int o = 16; o >= 8; o >>= 1)
 #pragma unroll
-    for (int o = 8; o >= 1; o >>= 1) {
+        for (int k = 0; k < 8; ++k)
+            v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+#pragma unroll
+    for (int o = 4; o >= 1; o >>= 1) {
         const bool up = lane & o;
 #pragma unroll
         for (int k = 0; k < o; ++k) {
@@ -126,7 +132,7 @@ __device__ __forceinline__ float transpose_sum16(float *v, int lane)
     return v[0];
 }
 
-template <int D>
+template <int D, int RW>
 __global__ void __launch_bounds__(kNarrowThreads, 1) sv_attention_narrow_kernel(const __grid_constant__ Maps maps, AttnParams p)
 {
     using N = NarrowCfg<D>;
@@ -136,7 +142,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) sv_attention_narrow_kernel(
     NarrowCtl &ctl = *reinterpret_cast<NarrowCtl *>(ring + kStages * kSlotBytes);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rows = p.T * p.G;  // of every segment, at most 64
-    const int ngroup = (rows + 15) / 16;
+    const int ngroup = (rows + RW - 1) / RW;
 
     if (smem_u32(smem) & 1023u) {
         if (tid == 0 && p.status)
@@ -176,7 +182,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) sv_attention_narrow_kernel(
     for (int x = tid * 16; x < N::kQ + N::kQC; x += kNarrowThreads * 16)
         *reinterpret_cast<uint4 *>(smem + x) = make_uint4(0, 0, 0, 0);
     fence_async_shared();
-    if (warp == 17) {
+    if (warp == kNarrowAux + 1) {
         tmem_alloc(&ctl.tmem, kTmemCols);
         tmem_relinquish();
     }
@@ -187,16 +193,16 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) sv_attention_narrow_kernel(
     const uint32_t tmem = ctl.tmem;
     Seg seg;
 
-    if (warp >= 16) {
+    if (warp >= kNarrowAux) {
         regs_dec<kNarrowRegsOther>();
-        if (warp == 16) {
+        if (warp == kNarrowAux) {
             if (lane == 0) {
                 Walk walk;
                 walk.start(p, u0, u1, ctl.start_b, ctl.start_ub);
                 produce<D, true, kStages, 1, N::kQ, kNarrowPanel>(p, maps, ctl, walk, smem, ring);
             }
             __syncwarp();
-        } else if (warp == 17) {
+        } else if (warp == kNarrowAux + 1) {
             // ---- MMA issuer ----
             constexpr uint32_t kTr = (1u << 15) | (1u << 16);  // both operands MN-major
             constexpr uint32_t idS = idesc_bf16_f32(kTile, kNarrowRows), idO = idS | kTr;
@@ -212,7 +218,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) sv_attention_narrow_kernel(
             const uint64_t dP = smem_desc(pw, 16, 1024, 128), dP8 = smem_desc(pw, N::kTerm, 512, 64);
             const uint32_t tmu = __shfl_sync(0xffffffffu, tmem, 0);
             const bool issue = elect_one();
-            uint32_t base = 0, nq = 0, nj = 0, nseg = 0, iseg = 0;
+            uint32_t base = 0, nq = 0, np0 = 0, np1 = 0, nseg = 0, iseg = 0;
             while (next_seg(ctl, iseg, seg)) {
                 if (seg.none())
                     continue;
@@ -223,7 +229,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) sv_attention_narrow_kernel(
                 ++nseg;
                 bool q8 = false;
                 auto scores = [&](int q) {
-                    const uint32_t s = (nj + (uint32_t)q) & 1u;
+                    const uint32_t s = (uint32_t)q & 1u;
                     const bool dr = draft && q == 0, first8 = !dr && !q8;
                     if (first8) {
                         await(ctl, &ctl.q_full, nq++);
@@ -233,7 +239,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) sv_attention_narrow_kernel(
                     const uint32_t st = __shfl_sync(0xffffffffu, f % kStages, 0);
                     await(ctl, &ctl.full[st], f / kStages);
                     tc_fence_after();
-                    const uint32_t d = tmu + 256 + 64 * __shfl_sync(0xffffffffu, s, 0);
+                    const uint32_t d = tmu + 384 + 64 * __shfl_sync(0xffffffffu, s, 0);
                     if (issue) {
                         if (dr) {
                             const uint64_t k0 = dK + st * (uint32_t)(kSlotBytes / 16);
@@ -259,14 +265,14 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) sv_attention_narrow_kernel(
                     __syncwarp();
                 };
                 auto product = [&](int q) {
-                    const uint32_t s = (nj + (uint32_t)q) & 1u;
+                    const uint32_t s = (uint32_t)q & 1u;
                     const bool dr = draft && q == 0, two = Fills<D, true>::two(dr);
                     const uint32_t f = base + Fills<D, true>::at(seg, q) + (two ? 1 : 0);
                     const uint32_t st = __shfl_sync(0xffffffffu, f % kStages, 0);
                     await(ctl, &ctl.full[st], f / kStages);
                     if (dr || seg.valid(seg.t0 + q) < kTile)
                         await(ctl, &ctl.fix[st], f / kStages);
-                    await(ctl, &ctl.p_full[s], (nj + (uint32_t)q) >> 1);
+                    await(ctl, &ctl.p_full[s], s ? np1++ : np0++);
                     if (dr) {  // only now: the last segment's has been read
                         if (lane < 4)
                             ctl.poison[lane] = ctl.poison_slot[st][lane];
@@ -277,8 +283,8 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) sv_attention_narrow_kernel(
                     tc_fence_after();
                     const uint32_t su = __shfl_sync(0xffffffffu, s, 0);
                     const uint32_t v = st * (uint32_t)(kSlotBytes / 16) + __shfl_sync(0xffffffffu, two ? 0u : (uint32_t)(kVoff / 16), 0);
-                    const uint32_t d = tmu, pb = su * (uint32_t)(N::kP / 16);
-                    const uint32_t acc = q >= 1;  // the segment's first product overwrites O^T
+                    const uint32_t d = tmu + 192 * su, pb = su * (uint32_t)(N::kP / 16);
+                    const uint32_t acc = q >= 2;  // a slot's first product of the segment overwrites O^T
                     if (issue) {
                         if (dr) {
 #pragma unroll
@@ -302,13 +308,12 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) sv_attention_narrow_kernel(
                     if (q + 2 < njobs)
                         scores(q + 2);
                 }
-                nj += (uint32_t)njobs;
                 base += Fills<D, true>::at(seg, seg.n - 1) + (Fills<D, true>::two(draft && seg.n == 1) ? 2 : 1);
             }
             if (issue)
                 tc_commit(&ctl.done);
             __syncwarp();
-        } else if (warp == 18) {
+        } else if (warp == kNarrowAux + 2) {
             clear_values<D, true, kStages>(p, ctl, ring, lane);
         } else {
             // ---- scales: the bytes of four of a segment's tiles are on their way while one's are written (the next
@@ -363,10 +368,12 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) sv_attention_narrow_kernel(
     } else {
         regs_inc<kNarrowRegsSoftmax>();
         const int wg = warp >> 2, wq = warp & 3, pt = tid & 127;
-        const int lo = 16 * wg, nrow = min(rows - lo, 16);  // this warpgroup's rows; none when nrow <= 0
+        const int group = wg >> 1, slot = wg & 1;
+        const int lo = RW * group, nrow = min(rows - lo, RW);  // this warpgroup's rows; none when nrow <= 0
         const uint32_t lanes = (uint32_t)(wq * 32) << 16;
-        const uint32_t tS = tmem + lanes + 256 + lo, tO = tmem + lanes + lo;
-        float *nmu = &ctl.nmu[lo], *fac = &ctl.fac[lo], *mu = &ctl.mu[lo];
+        const uint32_t tS = tmem + lanes + 384 + 64 * slot + lo, tO = tmem + lanes + 192 * slot + lo;
+        float *nmu = &ctl.nmu[slot][lo], *fac = &ctl.fac[slot][lo], *mu = &ctl.mu[slot][lo];
+        unsigned char *pslot = pw + slot * N::kP;
         uint32_t nj = 0, npois = 0, nseg = 0, nconv = 0;
         uint32_t base = 0;  // ring fills before this segment
         uint32_t iseg = 0;
@@ -424,12 +431,12 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) sv_attention_narrow_kernel(
                 bar_sync(1, kNarrowSoftmax);
                 continue;
             }
-            unsigned long long l2[8];  // this thread's sums of each row's weights
+            unsigned long long l2[RW / 2];  // this thread's sums of each row's weights
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
+            for (int k = 0; k < RW / 2; ++k)
                 l2[k] = 0;
             uint32_t vis = 0;  // this warpgroup's rows that see new token pt
-            if (draft) {
+            if (draft && slot == 0) {  // job 0 is slot 0's
                 unsigned long long tok = 0;  // tokens that see it
                 const int32_t *par = p.parent ? p.parent + (long long)seg.b * p.T : nullptr;
                 bool bad = false;
@@ -463,15 +470,17 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) sv_attention_narrow_kernel(
             }
 
 #pragma unroll 1
-            for (int q = 0; q < njobs; ++q, ++nj) {
-                const uint32_t s = nj & 1u, use = nj >> 1;  // buffers of S^T and P^T, and how often they were used
+            for (int q = slot; q < njobs; q += 2, ++nj) {
                 const bool dr = draft && q == 0;
-                await(ctl, &ctl.s_full[s], use);
+                await(ctl, &ctl.s_full[slot], nj);
                 tc_fence_after();
-                uint32_t x[16];
-                tmem_ld16_nowait(tS + 64 * s, x);
+                uint32_t x[RW];
+#pragma unroll
+                for (int k = 0; k < RW; k += 8)
+                    tmem_ld8_nowait(tS + k, x + k);
                 float f = p.c, ev = 0.0f, inv = 1.0f;
-                uint32_t see = 0xffffu;  // rows that see this thread's key
+                constexpr uint32_t kAll = (1u << RW) - 1u;
+                uint32_t see = kAll;  // rows that see this thread's key
                 if (dr) {
                     see = vis;
                 } else {
@@ -487,20 +496,20 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) sv_attention_narrow_kernel(
                 tmem_wait_ld();
                 // y = score * the key's factor + the exponent of the value's scale
 #pragma unroll
-                for (int k = 0; k < 16; k += 2)
+                for (int k = 0; k < RW; k += 2)
                     fma_pair(x[k], x[k + 1], f, f, ev, ev);
-                if (__any_sync(0xffffffffu, see != 0xffffu)) {
+                if (__any_sync(0xffffffffu, see != kAll)) {
 #pragma unroll
-                    for (int k = 0; k < 16; ++k)
+                    for (int k = 0; k < RW; ++k)
                         x[k] = (see >> k) & 1u ? x[k] : 0xff800000u;
                 }
-                if (q == 0) {  // first references: the best of four keys' scores
+                if (q < 2) {  // first references: the best of four keys' scores
                     if (lane == 0)
 #pragma unroll
-                        for (int k = 0; k < 16; k += 4)
+                        for (int k = 0; k < RW; k += 4)
                             *reinterpret_cast<uint4 *>(&ctl.part[wg][wq][k]) = make_uint4(x[k], x[k + 1], x[k + 2], x[k + 3]);
                     bar_sync(2 + wg, 128);
-                    if (pt < 16) {
+                    if (pt < RW) {
                         const float a = fmaxf(fmaxf(ctl.part[wg][0][pt], ctl.part[wg][1][pt]), fmaxf(ctl.part[wg][2][pt], ctl.part[wg][3][pt]));
                         // none of the four finite: start from 0
                         const float m = a > -INFINITY && a < INFINITY ? a + kNarrowMargin : 0.0f;
@@ -512,25 +521,29 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) sv_attention_narrow_kernel(
                 // z = y - mu + base, the logarithm of the weight
                 float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
-                for (int k = 0; k < 16; k += 4) {
+                for (int k = 0; k < RW; k += 4) {
                     const float4 n = *reinterpret_cast<const float4 *>(nmu + k);
                     add_pair(x[k], x[k + 1], n.x, n.y);
                     add_pair(x[k + 2], x[k + 3], n.z, n.w);
                     m0 = fmaxf(m0, fmaxf(__uint_as_float(x[k]), __uint_as_float(x[k + 1])));
                     m1 = fmaxf(m1, fmaxf(__uint_as_float(x[k + 2]), __uint_as_float(x[k + 3])));
                 }
+                if (nj > 0) {  // the slot's last product has read P and written O^T
+                    await(ctl, &ctl.o_full[slot], nj - 1);
+                    tc_fence_after();
+                }
                 if (any128(2 + wg, fmaxf(m0, m1) > kNarrowBase + kNarrowSlack)) {
                     // some row has outgrown its reference: reduce the maxima, rescale
                     int mine = 0;
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) {
+                    for (int k = 0; k < RW; ++k) {
                         const int r = __reduce_max_sync(0xffffffffu, ordered(__uint_as_float(x[k])));
                         mine = lane == k ? r : mine;
                     }
-                    if (lane < 16)
+                    if (lane < RW)
                         ctl.part[wg][wq][lane] = unordered(mine);
                     bar_sync(2 + wg, 128);
-                    if (pt < 16) {
+                    if (pt < RW) {
                         // the largest z, and how far the reference moves: up only
                         const float z = fmax_nan(fmax_nan(ctl.part[wg][0][pt], ctl.part[wg][1][pt]), fmax_nan(ctl.part[wg][2][pt], ctl.part[wg][3][pt]));
                         const float d = fmax_nan(z - kNarrowBase, 0.0f);
@@ -540,155 +553,176 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) sv_attention_narrow_kernel(
                     }
                     bar_sync(2 + wg, 128);
 #pragma unroll
-                    for (int k = 0; k < 16; k += 4) {
+                    for (int k = 0; k < RW; k += 4) {
                         const float4 d = *reinterpret_cast<const float4 *>(fac + k);
                         add_pair(x[k], x[k + 1], d.x, d.y);
                         add_pair(x[k + 2], x[k + 3], d.z, d.w);
                         l2[k / 2] = mul2(l2[k / 2], pack2(ex2(d.x), ex2(d.y)));
                         l2[k / 2 + 1] = mul2(l2[k / 2 + 1], pack2(ex2(d.z), ex2(d.w)));
                     }
-                    if (q > 0) {  // the last tile's product is complete before O^T is rescaled
-                        await(ctl, &ctl.o_full[(nj - 1) & 1u], (nj - 1) >> 1);
-                        tc_fence_after();
+                    if (q >= 2) {
 #pragma unroll 1
-                        for (int c0 = 0; c0 < 192; c0 += 64) {
-                            uint32_t o[16];
-                            tmem_ld16_nowait(tO + c0, o);
-                            tmem_wait_ld();
+                        for (int c0 = 0; c0 < 192; c0 += 64)
+#pragma unroll 1
+                            for (int c1 = 0; c1 < RW; c1 += 8) {
+                                uint32_t o[8];
+                                tmem_ld8_nowait(tO + c0 + c1, o);
+                                tmem_wait_ld();
 #pragma unroll
-                            for (int k = 0; k < 16; ++k)
-                                o[k] = __float_as_uint(__uint_as_float(o[k]) * ex2(fac[k]));
-                            tmem_st16(tO + c0, o);
-                        }
+                                for (int k = 0; k < 8; ++k)
+                                    o[k] = __float_as_uint(__uint_as_float(o[k]) * ex2(fac[c1 + k]));
+                                tmem_st8(tO + c0 + c1, o);
+                            }
                         tmem_wait_st();
                     }
                 }
-                if (use > 0)  // the buffer's last product has read P
-                    await(ctl, &ctl.o_full[s], use - 1);
-                // w = 2^z, summed and rounded into P^T
+                // w = 2^z, summed and rounded into P^T, 8 rows at a time
                 const unsigned long long inv2 = pack2(inv, inv);
-                unsigned char *pslot = pw + s * N::kP;
-                uint32_t t[12];
 #pragma unroll
-                for (int k = 0; k < 16; k += 4) {
-                    float w[4];
+                for (int g = 0; g < RW; g += 8) {
+                    uint32_t t[6];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        w[j] = ex2(__uint_as_float(x[k + j]));
-                    l2[k / 2] = fma2(pack2(w[0], w[1]), inv2, l2[k / 2]);
-                    l2[k / 2 + 1] = fma2(pack2(w[2], w[3]), inv2, l2[k / 2 + 1]);
-                    if (dr) {
-                        x[k / 2] = pack_bf16(w[0], w[1]);
-                        x[k / 2 + 1] = pack_bf16(w[2], w[3]);
-                    } else {
-                        three_terms(w, t[k / 4], t[4 + k / 4], t[8 + k / 4]);
+                    for (int k = g; k < g + 8; k += 4) {
+                        float w[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            w[j] = ex2(__uint_as_float(x[k + j]));
+                        l2[k / 2] = fma2(pack2(w[0], w[1]), inv2, l2[k / 2]);
+                        l2[k / 2 + 1] = fma2(pack2(w[2], w[3]), inv2, l2[k / 2 + 1]);
+                        if (dr) {
+                            x[k] = pack_bf16(w[0], w[1]);
+                            x[k + 1] = pack_bf16(w[2], w[3]);
+                        } else {
+                            three_terms(w, t[(k - g) / 4], t[2 + (k - g) / 4], t[4 + (k - g) / 4]);
+                        }
+                    }
+                    const int c = (lo + g) / 8;  // which 8 rows of 64
+                    if (dr) {  // key pt's 128 bytes, swizzled
+                        *reinterpret_cast<uint4 *>(pslot + pt * 128 + ((c ^ (pt & 7)) * 16)) = make_uint4(x[g], x[g + 1], x[g + 4], x[g + 5]);
+                    } else {  // its 64 bytes in each of the three
+#pragma unroll
+                        for (int part = 0; part < 3; ++part)
+                            *reinterpret_cast<uint2 *>(pslot + part * N::kTerm + pt * 64 + (((c >> 1) ^ ((pt >> 1) & 3)) * 16) + (c & 1) * 8) =
+                                make_uint2(t[2 * part], t[2 * part + 1]);
                     }
                 }
-                if (dr) {  // row pt of 128 bytes, swizzled
+                if (dr) {  // the new tokens' product writes the first part of O^T only
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        *reinterpret_cast<uint4 *>(pslot + pt * 128 + (((2 * wg + j) ^ (pt & 7)) * 16)) =
-                            make_uint4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
-                    // their product writes the first part of O^T only
-#pragma unroll
-                    for (int k = 0; k < 16; ++k)
-                        x[k] = 0;
-                    tmem_st16(tO + 64, x);
-                    tmem_st16(tO + 128, x);
+                    for (int k = 0; k < RW; k += 8) {
+                        const uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                        tmem_st8(tO + 64 + k, zero);
+                        tmem_st8(tO + 128 + k, zero);
+                    }
                     tmem_wait_st();
-                } else {  // row pt of 64 bytes in each of the three
-#pragma unroll
-                    for (int part = 0; part < 3; ++part)
-                        *reinterpret_cast<uint4 *>(pslot + part * N::kTerm + pt * 64 + ((wg ^ ((pt >> 1) & 3)) * 16)) =
-                            make_uint4(t[4 * part], t[4 * part + 1], t[4 * part + 2], t[4 * part + 3]);
                 }
                 fence_async_shared();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(&ctl.p_full[s]);
+                    mbar_arrive(&ctl.p_full[slot]);
             }
             if (!none)
                 base += Fills<D, true>::at(seg, seg.n - 1) + (Fills<D, true>::two(draft && seg.n == 1) ? 2 : 1);
 
-            // ---- epilogue ----
-            if (!none)
-                await(ctl, &ctl.o_full[(nj - 1) & 1u], (nj - 1) >> 1);
-            float lv[16];
+            // ---- epilogue: the slots of these rows ----
+            const bool has = slot < njobs;
+            if (has)
+                await(ctl, &ctl.o_full[slot], nj - 1);
+            float lv[RW];
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
+            for (int k = 0; k < RW / 2; ++k)
                 unpack2(l2[k], lv[2 * k], lv[2 * k + 1]);
             if (draft) {
                 await(ctl, &ctl.poison_full, npois++);
                 if ((ctl.poison[wq] >> lane) & 1u) {  // new token pt's values are not finite
 #pragma unroll
-                    for (int k = 0; k < 16; ++k)
+                    for (int k = 0; k < RW; ++k)
                         lv[k] = (vis >> k) & 1u ? nan_f() : lv[k];
                 }
             }
-            const float sum = transpose_sum16(lv, lane);
-            if (lane < 16)
-                ctl.part[wg][wq][lane] = sum;
+#pragma unroll
+            for (int k = 0; k < RW; k += 8) {
+                const float sum = transpose_sum8(lv + k, lane);
+                if (lane < 8)
+                    ctl.part[wg][wq][k + lane] = sum;
+            }
+            tc_fence_before();
             bar_sync(2 + wg, 128);
-            const bool direct = seg.whole();
-            float *slot = p.pieces + (size_t)(2 * blockIdx.x + (seg.first ? 0 : 1)) * p.rm * (D + 4);
             if (pt < nrow) {
+                ctl.l[slot][lo + pt] = poison || seg.bad ? nan_f() : (ctl.part[wg][0][pt] + ctl.part[wg][1][pt]) + (ctl.part[wg][2][pt] + ctl.part[wg][3][pt]);
+                if (!has)
+                    mu[pt] = -INFINITY;
+            }
+            bar_sync(6 + group, 256);  // every slot's product and sums are complete
+            tc_fence_after();
+            const bool direct = seg.whole();
+            float *piece = p.pieces + (size_t)(2 * blockIdx.x + (seg.first ? 0 : 1)) * p.rm * (D + 4);
+            if (slot == 0 && pt < nrow) {
                 const int r = lo + pt;
-                const float l = poison || seg.bad ? nan_f() : (ctl.part[wg][0][pt] + ctl.part[wg][1][pt]) + (ctl.part[wg][2][pt] + ctl.part[wg][3][pt]);
-                const float R = none ? -INFINITY : mu[pt] - kNarrowBase;
-                float fa = 1.0f;
+                const float ma = ctl.mu[0][r], mb = ctl.mu[1][r], mn = fmax_nan(ma, mb);
+                float fa = ma == -INFINITY ? 0.0f : ex2(ma - mn), fb = mb == -INFINITY ? 0.0f : ex2(mb - mn);
+                const float la = ctl.l[0][r], lb = ctl.l[1][r];
+                const float l = (la != la ? la : la * fa) + (lb != lb ? lb : lb * fb), R = mn - kNarrowBase;
                 if (direct) {
-                    fa = l == 0.0f ? 0.0f : 1.0f / l;
+                    const float scl = l == 0.0f ? 0.0f : 1.0f / l;
+                    fa *= scl;
+                    fb *= scl;
                     if (p.lse) {
                         const int Rg = seg.row0 + r, tok = Rg / p.G;
                         p.lse[(size_t)tok * p.Hq + seg.h * p.G + (Rg - tok * p.G)] = l == 0.0f ? -INFINITY : (R + log2f(l)) * 0.69314718055994531f;
                     }
                 } else {
-                    *reinterpret_cast<float2 *>(slot + (size_t)p.rm * D + r * 2) = make_float2(R, l);
+                    *reinterpret_cast<float2 *>(piece + (size_t)p.rm * D + r * 2) = make_float2(R, l);
                 }
-                fac[pt] = l != l ? l : fa;  // NaN reaches every column
+                ctl.fac[0][r] = l != l ? l : fa;  // NaN reaches every column
+                ctl.fac[1][r] = fb;
             }
             if (seg.bad && p.status && tid == 0)
                 atomicOr(p.status, SV_ATTN_BAD_LEN);
-            bar_sync(2 + wg, 128);
-            tc_fence_after();
-            if (D == 128 || wq < 2) {  // thread = channel
-                float o[16];
-                if (!none) {
-                    uint32_t y[48];
-#pragma unroll
-                    for (int part = 0; part < 3; ++part)
-                        tmem_ld16_nowait(tO + 64 * part, y + 16 * part);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int k = 0; k < 16; ++k)
-                        o[k] = fac[k] * ((__uint_as_float(y[k]) + __uint_as_float(y[16 + k])) + __uint_as_float(y[32 + k]));
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 16; ++k)
-                        o[k] = seg.bad ? nan_f() : 0.0f;
-                }
+            bar_sync(6 + group, 256);
+            if (D == 128 || wq < 2) {  // thread = channel; the slots write 8 rows in turn
                 const int d = 32 * wq + lane;
-                if (direct) {
-                    int tok = (seg.row0 + lo) / p.G, g = seg.row0 + lo - tok * p.G;
-                    __nv_bfloat16 *dst = p.out + ((size_t)tok * p.Hq + seg.h * p.G + g) * D + d;
-                    const int wrap = (p.Hq - p.G) * D;  // from the last row of a token to the next one's first
+#pragma unroll 1
+                for (int r0 = lo + 8 * slot; r0 < lo + nrow; r0 += 16) {
+                    float o[8];
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        if (k < nrow)
-                            *dst = __float2bfloat16(o[k]);
-                        dst += D;
-                        if (++g == p.G) {
-                            g = 0;
-                            dst += wrap;
+                    for (int k = 0; k < 8; ++k)
+                        o[k] = none && seg.bad ? nan_f() : 0.0f;
+#pragma unroll 1
+                    for (int from = 0; from < min(2, njobs); ++from) {
+                        uint32_t y[24];
+#pragma unroll
+                        for (int part = 0; part < 3; ++part)
+                            tmem_ld8_nowait(tmem + lanes + 192 * from + 64 * part + r0, y + 8 * part);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const float a = ctl.fac[from][r0 + k];
+                            const float v = (__uint_as_float(y[k]) + __uint_as_float(y[8 + k])) + __uint_as_float(y[16 + k]);
+                            o[k] += a == 0.0f ? 0.0f : a * v;
                         }
                     }
-                } else {
-                    float *dst = slot + (size_t)lo * D + d;
+                    if (direct) {
+                        int tok = (seg.row0 + r0) / p.G, g = seg.row0 + r0 - tok * p.G;
+                        __nv_bfloat16 *dst = p.out + ((size_t)tok * p.Hq + seg.h * p.G + g) * D + d;
+                        const int wrap = (p.Hq - p.G) * D;  // from the last row of a token to the next one's first
 #pragma unroll
-                    for (int k = 0; k < 16; ++k)
-                        if (k < nrow)
-                            dst[k * D] = o[k];
+                        for (int k = 0; k < 8; ++k) {
+                            if (r0 + k < rows)
+                                *dst = __float2bfloat16(o[k]);
+                            dst += D;
+                            if (++g == p.G) {
+                                g = 0;
+                                dst += wrap;
+                            }
+                        }
+                    } else {
+                        float *dst = piece + (size_t)r0 * D + d;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            if (r0 + k < rows)
+                                dst[k * D] = o[k];
+                    }
                 }
             }
             tc_fence_before();
@@ -700,7 +734,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) sv_attention_narrow_kernel(
     }
     finish<kStages, 1>(p, ctl);
     tc_fence_after();
-    if (warp == 17)
+    if (warp == kNarrowAux + 1)
         tmem_dealloc(tmem, kTmemCols);
 }
 

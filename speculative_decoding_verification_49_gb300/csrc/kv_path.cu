@@ -12,10 +12,11 @@
 // plus 1 when f > 0.75 (448 = 1.75 * 2^8), read off the bf16 bits.  A lane holds
 // 8 elements (one 16-byte load), D / 8 lanes share a vector (rounded up to a
 // power of two, the rest idle) and find its maximum by xor shuffles.
-// A cluster of CTAs serves one sequence in all planes, so one launch does the
-// copy and the new length: every CTA reads cache_len, the cluster barrier's
-// arrival follows, and one thread writes the length after the barrier, which
-// allows out_len == cache_len.
+// The vectors of all sequences, planes and rows form one line that is cut into
+// equal stretches, one per CTA, so that the few sequences with many accepted rows do not
+// make a tail (a cluster of CTAs a sequence took 48 us on 256 tree paths in 56
+// planes).  Every CTA scans the batch's counts for that.  One launch, when the new lengths go to an
+// array of their own; a second one, after every CTA has read them, when they replace the old.
 // Bound: HBM on rows * heads * (2 D in + D + 1 out) bytes; at a serving batch the
 // rows are few, so launch and load latency count first.
 //
@@ -40,6 +41,7 @@ using namespace sv;
 
 constexpr int kPathThreads = 256;
 constexpr int kPathUnroll = 4;  // vectors of a lane group in flight
+constexpr int kPathCtas = 608;  // four on each of 152 SMs
 constexpr int kPathMaxT = 1024;
 constexpr int kReadThreads = 256;
 constexpr int kReadUnroll = 4;  // 16-code chunks of a thread in flight
@@ -69,116 +71,240 @@ __device__ __forceinline__ float pow2i(int e)
     return __int_as_float((e + 127) << 23);
 }
 
-// 8 bf16 (four words) times s as 8 e4m3 codes; NaN and infinities become NaN.
-__device__ __forceinline__ uint2 quantise8(const unsigned *w, float s)
+// Two floats as two e4m3 codes (the low half of the result); NaN becomes the NaN code.
+__device__ __forceinline__ unsigned codes2(float lo, float hi)
 {
-    unsigned out[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        unsigned c[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const unsigned u = w[2 * i + j];
-            float lo = __uint_as_float(u << 16), hi = __uint_as_float(u & 0xffff0000u);
-            lo = (u & 0x7f80u) == 0x7f80u ? __int_as_float(0x7fc00000) : lo * s;
-            hi = (u & 0x7f800000u) == 0x7f800000u ? __int_as_float(0x7fc00000) : hi * s;
-            c[j] = __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
-        }
-        out[i] = c[0] | (c[1] << 16);
-    }
-    return make_uint2(out[0], out[1]);
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
 }
 
-// Grid: x = CTAs of a sequence (one cluster), y = sequence.  LPV lanes serve one vector.
-template <bool E4M3, int LPV>
-__global__ void __launch_bounds__(kPathThreads) sv_kv_path_kernel(PathParams k)
+// 8 finite bf16 (four words) times s as 8 e4m3 codes.
+__device__ __forceinline__ uint2 quantise8(const unsigned *w, float s)
 {
-    grid_dependency_wait();
-    const int b = blockIdx.y;
-    const int len = __ldg(&k.cache_len[b]), a = __ldg(&k.nacc[b]);
-    int rows = a < 0 ? 0 : k.lead + a, bits = 0;
-    if (a >= 0) {
-        if (a > k.T - k.lead)
-            bits = SV_KV_BAD_COUNT;
-        else if (len < 0 || len > k.max_len - rows)
-            bits = SV_KV_OVERFLOW;
+    unsigned c[4];
+    const unsigned long long s2 = pack2(s, s);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float lo, hi;
+        unpack2(mul2(pack2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u)), s2), lo, hi);
+        c[j] = codes2(lo, hi);
     }
-    __shared__ int32_t src_row[kPathMaxT];  // scratch row of each committed row
-    bool bad = false;
-    if (!bits)
-        for (int i = threadIdx.x; i < rows; i += kPathThreads) {
-            int r = i;
-            if (i >= k.lead && k.path)
-                r = __ldg(&k.path[(size_t)b * k.T + (i - k.lead)]);
-            bad |= (unsigned)r >= (unsigned)k.T;
-            src_row[i] = r;
+    return make_uint2(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410));
+}
+
+// The words with NaN in the place of infinities (a vector that holds either takes this way).
+__device__ __forceinline__ void nan_for_inf(unsigned *w)
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if ((w[j] & 0x7f80u) == 0x7f80u)
+            w[j] |= 0x40u;
+        if ((w[j] & 0x7f800000u) == 0x7f800000u)
+            w[j] |= 0x400000u;
+    }
+}
+
+// Largest 16-bit magnitudes of four words, even and odd elements apart; without the non-finite ones.
+__device__ __forceinline__ unsigned max_words(const unsigned *w, bool finite_only)
+{
+    unsigned m = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        unsigned x = w[j] & 0x7fff7fffu;
+        if (finite_only) {
+            if ((x & 0xffffu) >= 0x7f80u)
+                x &= 0xffff0000u;
+            if (x >= 0x7f800000u)
+                x &= 0xffffu;
         }
-    if (__syncthreads_or(bad))
-        bits = SV_KV_BAD_PATH;
-    if (bits)
-        rows = 0;
-    // every thread of the cluster has read the old length once this barrier completes
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        m = __vmaxu2(m, x);
+    }
+    return m;
+}
+
+// Rows that sequence b commits by its counts, and the error bits that they raise.
+__device__ __forceinline__ int path_rows(const PathParams &k, int b, int &len, int &bits)
+{
+    const int a = __ldg(&k.nacc[b]);
+    len = __ldg(&k.cache_len[b]);
+    bits = 0;
+    if (a < 0)
+        return 0;
+    if (a > k.T - k.lead) {
+        bits = SV_KV_BAD_COUNT;
+        return 0;
+    }
+    if (len < 0 || len > k.max_len - k.lead - a) {
+        bits = SV_KV_OVERFLOW;
+        return 0;
+    }
+    return k.lead + a;
+}
+
+// Scratch row of committed row i, -1 outside the scratch.
+__device__ __forceinline__ int path_src(const PathParams &k, int b, int i)
+{
+    const int r = i >= k.lead && k.path ? __ldg(&k.path[(size_t)b * k.T + (i - k.lead)]) : i;
+    return (unsigned)r < (unsigned)k.T ? r : -1;
+}
+
+// Sequence b's new length and its error bits.
+__device__ __forceinline__ void path_length(const PathParams &k, int b)
+{
+    int len, bits, rows = path_rows(k, b, len, bits);
+    if (k.path)
+        for (int i = k.lead; i < rows; ++i)
+            if (path_src(k, b, i) < 0) {
+                rows = 0;
+                bits = SV_KV_BAD_PATH;
+            }
+    k.out_len[b] = len + rows;
+    if (bits && k.status)
+        atomicOr(k.status, bits);
+}
+
+__global__ void __launch_bounds__(kPathThreads) sv_kv_path_len_kernel(PathParams k)
+{
+    grid_dependency_wait();  // every copy has read cache_len
+    const int b = blockIdx.x * kPathThreads + threadIdx.x;
+    if (b < k.B)
+        path_length(k, b);
+}
+
+// LPV lanes serve one vector.
+template <bool E4M3, int LPV>
+__global__ void __launch_bounds__(kPathThreads, 4) sv_kv_path_kernel(PathParams k)
+{
+    __shared__ int32_t src_row[kPathMaxT];  // scratch row of each committed row
+    __shared__ int warp_sum[kPathThreads / 32];
+    __shared__ int start_b;
+    __shared__ long long start_v;
+    grid_dependency_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const unsigned heads = (unsigned)k.heads, per_row = (unsigned)k.P * heads;  // vectors of a row, in all planes
+    // rows of the batch before this thread's sequences, and in all
+    const int chunk = (k.B + kPathThreads - 1) / kPathThreads;
+    const int bs = min(k.B, (int)threadIdx.x * chunk), be = min(k.B, bs + chunk);
+    int mine = 0, len, bits;
+    for (int b = bs; b < be; ++b)
+        mine += path_rows(k, b, len, bits);
+    if (blockIdx.x == 0 && k.out_len != k.cache_len)
+        for (int b = bs; b < be; ++b)
+            path_length(k, b);
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, incl, o);
+        incl += lane >= o ? x : 0;
+    }
+    if (lane == 31)
+        warp_sum[warp] = incl;
+    __syncthreads();
+    int before = incl - mine, total = 0;
+#pragma unroll
+    for (int w = 0; w < kPathThreads / 32; ++w) {
+        before += w < warp ? warp_sum[w] : 0;
+        total += warp_sum[w];
+    }
+    const long long all = (long long)total * per_row;
+    const long long v0 = all * blockIdx.x / gridDim.x, v1 = all * (blockIdx.x + 1) / gridDim.x;
+    long long at = (long long)before * per_row;
+    if (v0 < v1 && v0 >= at && v0 < at + (long long)mine * per_row)
+        for (int b = bs; b < be; ++b) {
+            const long long next = at + (long long)path_rows(k, b, len, bits) * per_row;
+            if (v0 >= at && v0 < next) {
+                start_b = b;
+                start_v = at;
+            }
+            at = next;
+        }
+    __syncthreads();
+    if (v0 >= v1)
+        return;
 
     const unsigned sub = threadIdx.x % LPV;
     const bool active = (int)sub * 8 < k.D;
-    const unsigned nvec = (unsigned)k.P * (unsigned)rows * (unsigned)k.heads;  // below 2^31
-    const unsigned per = kPathThreads / LPV * gridDim.x;  // vectors the cluster takes at a time
-    const unsigned first = blockIdx.x * (kPathThreads / LPV) + threadIdx.x / LPV;
-    const unsigned hr = (unsigned)k.heads * (unsigned)rows;
+    constexpr unsigned kPer = kPathThreads / LPV;  // vectors that the CTA takes at a time
+    const size_t src_plane = (size_t)k.B * k.T * heads * k.D * 2, vec_plane = (size_t)k.B * k.max_len * heads;
     bool nonfinite = false;
-    for (unsigned v0 = first - threadIdx.x / LPV; v0 < nvec; v0 += per * kPathUnroll) {  // uniform over the CTA
-        uint4 x[kPathUnroll];
-        size_t dst[kPathUnroll];
-#pragma unroll
-        for (int j = 0; j < kPathUnroll; ++j) {
-            const unsigned v = v0 + threadIdx.x / LPV + j * per;
-            x[j] = make_uint4(0, 0, 0, 0);
-            if (v < nvec) {
-                const unsigned p = v / hr, ih = v - p * hr, i = ih / (unsigned)k.heads, h = ih - i * (unsigned)k.heads;
-                const size_t seq = (size_t)p * k.B + b;
-                dst[j] = (seq * k.max_len + (size_t)(len + (int)i)) * k.heads + h;
-                if (active)
-                    x[j] = __ldcs(reinterpret_cast<const uint4 *>(
-                        k.rows + ((((seq * k.T + src_row[i]) * k.heads + h) * k.D) + sub * 8) * 2));
-            }
+    long long seq = start_v;  // first vector of sequence b
+    for (int b = start_b; seq < v1; ++b) {
+        const int rows = path_rows(k, b, len, bits);
+        const unsigned hr = heads * (unsigned)rows;
+        const long long next = seq + (long long)rows * per_row;
+        __syncthreads();  // the last sequence's rows have been used
+        bool bad = false;
+        for (int i = threadIdx.x; i < rows; i += kPathThreads) {
+            src_row[i] = path_src(k, b, i);
+            bad |= src_row[i] < 0;
         }
+        bad = __syncthreads_or(bad);
+        const unsigned lo = (unsigned)((v0 > seq ? v0 : seq) - seq), hi = (unsigned)((v1 < next ? v1 : next) - seq);
+        seq = next;
+        if (bad || rows == 0)
+            continue;
+        // vector v = (plane, row, head); the steps by kPer are taken digit by digit, a division each only here
+        unsigned v = lo + threadIdx.x / LPV;
+        unsigned pl = v / hr, ro = (v - pl * hr) / heads, he = v - pl * hr - ro * heads;
+        const unsigned dp = kPer / hr, dr = (kPer - dp * hr) / heads, dh = kPer - dp * hr - dr * heads;
+        const unsigned char *src = k.rows + (size_t)b * k.T * heads * k.D * 2 + sub * 16;
+        const size_t vec0 = ((size_t)b * k.max_len + len) * heads;
+        for (unsigned u = lo; u < hi; u += kPer * kPathUnroll) {  // uniform over the CTA
+            uint4 x[kPathUnroll];
+            size_t dst[kPathUnroll];
 #pragma unroll
-        for (int j = 0; j < kPathUnroll; ++j) {
-            const unsigned v = v0 + threadIdx.x / LPV + j * per;
-            if constexpr (E4M3) {
-                const unsigned w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-                unsigned m = 0;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const unsigned lo = w[q] & 0x7fffu, hi = (w[q] >> 16) & 0x7fffu;
-                    nonfinite |= lo >= 0x7f80u || hi >= 0x7f80u;
-                    m = max(m, max(lo >= 0x7f80u ? 0u : lo, hi >= 0x7f80u ? 0u : hi));
-                }
-#pragma unroll
-                for (int o = LPV / 2; o >= 1; o >>= 1)
-                    m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-                const int e = scale_exponent(m);
-                if (v < nvec) {
+            for (int j = 0; j < kPathUnroll; ++j) {
+                x[j] = make_uint4(0, 0, 0, 0);
+                dst[j] = 0;
+                if (v + j * kPer < hi) {
+                    dst[j] = vec0 + pl * vec_plane + ro * heads + he;
                     if (active)
-                        *reinterpret_cast<uint2 *>(k.cache + dst[j] * k.D + sub * 8) = quantise8(w, pow2i(-e));
-                    if (sub == 0)
-                        k.scale[dst[j]] = (uint8_t)(e + 127);
+                        x[j] = __ldcs(reinterpret_cast<const uint4 *>(src + pl * src_plane + ((size_t)src_row[ro] * heads + he) * k.D * 2));
                 }
-            } else if (v < nvec && active) {
-                *reinterpret_cast<uint4 *>(k.cache + (dst[j] * k.D + sub * 8) * 2) = x[j];
+                he += dh;
+                ro += dr;
+                if (he >= heads) {
+                    he -= heads;
+                    ++ro;
+                }
+                pl += dp;
+                if (ro >= (unsigned)rows) {
+                    ro -= (unsigned)rows;
+                    ++pl;
+                }
             }
+#pragma unroll
+            for (int j = 0; j < kPathUnroll; ++j) {
+                const bool in = v + j * kPer < hi;
+                if constexpr (E4M3) {
+                    unsigned w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+                    unsigned m = max_words(w, false);
+                    const bool nf = (m & 0xffffu) >= 0x7f80u || m >= 0x7f800000u;
+                    if (__any_sync(0xffffffffu, nf)) {
+                        nonfinite |= nf;
+                        m = max_words(w, true);
+                        nan_for_inf(w);
+                    }
+#pragma unroll
+                    for (int o = LPV / 2; o >= 1; o >>= 1)
+                        m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+                    const int e = scale_exponent(max(m & 0xffffu, m >> 16));
+                    if (in) {
+                        if (active)
+                            *reinterpret_cast<uint2 *>(k.cache + dst[j] * k.D + sub * 8) = quantise8(w, pow2i(-e));
+                        if (sub == 0)
+                            k.scale[dst[j]] = (uint8_t)(e + 127);
+                    }
+                } else if (in && active) {
+                    *reinterpret_cast<uint4 *>(k.cache + (dst[j] * k.D + sub * 8) * 2) = x[j];
+                }
+            }
+            v += kPer * kPathUnroll;
         }
     }
     if (nonfinite && k.status)
         atomicOr(k.status, SV_KV_NONFINITE);
-    __syncwarp();
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-    if (blockIdx.x == 0 && threadIdx.x == 0) {
-        k.out_len[b] = len + rows;
-        if (bits && k.status)
-            atomicOr(k.status, bits);
-    }
 }
 
 struct ReadParams {
@@ -305,24 +431,24 @@ extern "C" sv_status spec_verify_kv_commit_path(const void *rows, void *cache, u
         return SV_ERR_TOO_LARGE;
     PathParams k = {static_cast<const unsigned char *>(rows), static_cast<unsigned char *>(cache), scale, cache_len,
                     out_len, num_accepted, path, status, planes, B, T, lead, max_len, heads, head_dim};
-    // CTAs of a sequence: enough that the batch covers the SMs twice, none without a round of vectors
-    int cs = 8;
-    while (cs > 1 && ((long long)B * cs > 1216 || (long long)planes * T * heads * head_dim <= (long long)(cs / 2) * kPathThreads * 8))
-        cs >>= 1;
-    cudaLaunchAttribute attr[2];
+    // a CTA for every pass of vectors that there can be, four to an SM at most
+    const int lanes = head_dim <= 16 ? 2 : head_dim <= 32 ? 4 : head_dim <= 64 ? 8 : head_dim <= 128 ? 16 : 32;
+    const long long passes = ((long long)planes * T * heads * lanes + kPathThreads - 1) / kPathThreads * B;
+    cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)cs;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)cs, (unsigned)B);
+    cfg.gridDim = dim3((unsigned)(passes < 1 ? 1 : passes < kPathCtas ? passes : kPathCtas));
     cfg.blockDim = dim3(kPathThreads);
     cfg.stream = static_cast<cudaStream_t>(stream);
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    if ((format == SV_KV_E4M3 ? launch_path<true>(cfg, k) : launch_path<false>(cfg, k)) != cudaSuccess) {
+    cfg.numAttrs = 1;
+    cudaError_t e = format == SV_KV_E4M3 ? launch_path<true>(cfg, k) : launch_path<false>(cfg, k);
+    if (e == cudaSuccess && out_len == cache_len) {
+        cfg.gridDim = dim3((unsigned)((B + kPathThreads - 1) / kPathThreads));
+        e = cudaLaunchKernelEx(&cfg, sv_kv_path_len_kernel, k);
+    }
+    if (e != cudaSuccess) {
         cudaGetLastError();
         return SV_ERR_CUDA;
     }

@@ -110,7 +110,10 @@ struct AttnParams {
     long long q_sb, q_st;
     int B, T, Hq, H, G, L, Lp;
     int has_new, max_len;
+    int nb;                 // sequences on the line: B, or none (the prefix alone)
+    int join_all;           // every row has parts elsewhere: nothing is written directly
     int seg_cost;           // what a segment counts beside its tiles, in tiles
+    int prefix_cost;        // the same of the line that the prefix segments are on (for the joining kernel)
     int tma_q;              // a sequence's rows fit one slot: their queries come by TMA
     int nbp, ntp, UP;       // prefix: row blocks and tiles a head, units in all
     int nbs;                // row blocks of a sequence's rows
@@ -481,8 +484,8 @@ template <int kThr, class Ct> __device__ __forceinline__ void find_stretch(const
     // ---- units of every sequence: this CTA's stretch and where it starts ----
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int per = p.H * p.nbs;  // segments of a sequence
-    const int chunk = cdiv(p.B, kThr);
-    const int bs = min(p.B, tid * chunk), be = min(p.B, bs + chunk);
+    const int chunk = cdiv(p.nb, kThr);
+    const int bs = min(p.nb, tid * chunk), be = min(p.nb, bs + chunk);
     int mine = 0;
     for (int b = bs; b < be; ++b)
         mine += (p.seg_cost + tiles_of(p, clean_len(p, raw_len(p, b)).n));
@@ -525,8 +528,8 @@ template <int kThr, class Ct> __device__ __forceinline__ void find_stretch(const
                     p.seg_start[b] = ub;
                 ub = next;
             }
-        if (blockIdx.x == 0 && tid == 0)
-            p.seg_start[p.B] = U;
+        if (blockIdx.x == 0 && tid == 0 && p.nb > 0)
+            p.seg_start[p.nb] = U;
     }
     __syncthreads();
 }
@@ -558,7 +561,7 @@ __device__ __forceinline__ void produce(const AttnParams &p, const Maps &maps, C
     };
     while (ok) {
         const bool more = walk.next(p, seg);
-        if (!cut_known && p.UP == 0) {
+        if (!cut_known && !p.join_all) {
             // the segment that this CTA's stretch starts inside of, for the joining kernel: the stretch starts at its tile t0
             const bool cut = more && seg.t0 > 0;
             p.cuts[2 * blockIdx.x] = make_int4(cut ? seg.row0 : -1, cut ? seg.nrows : 0, cut ? walk.u0 - seg.t0 : 0, cut ? seg.nt : 0);
@@ -706,6 +709,17 @@ template <int kStages, int kQBufs, class Ct> __device__ __forceinline__ void fin
         }
         __syncthreads();
     }
+}
+
+// Where a segment's partial rows go: O [rows][D], then (R, l) of each; rows is the slot's.
+template <int D> __device__ __forceinline__ float *part_of(const AttnParams &p, const Seg &seg, int &rows)
+{
+    if (!seg.whole()) {
+        rows = p.rm;
+        return p.pieces + (size_t)(2 * blockIdx.x + (seg.first ? 0 : 1)) * rows * (D + 4);
+    }
+    rows = seg.prefix ? p.rp : p.rs;
+    return (seg.prefix ? p.whole_p : p.whole_s) + (size_t)seg.id * rows * (D + 4);
 }
 
 // Largest magnitude (15 bits) of the finite ones among 8 bf16.
@@ -1281,20 +1295,13 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
             if (active) {
                 const float R = mu - C::kBase;  // -inf when nothing was seen
                 const bool valid_row = r < rows;
-                const bool direct = p.UP == 0 && seg.whole();
+                const bool direct = !p.join_all && seg.whole();
                 const int cs = pair ? 0 : s * (D / 2), ce = pair ? D : cs + D / 2;
                 float *part = nullptr;
                 if (!direct) {
                     const int rr = r + (pair ? kTile * s : 0);
-                    float *slot;
                     int nr;
-                    if (!seg.whole()) {
-                        nr = p.rm;
-                        slot = p.pieces + (size_t)(2 * blockIdx.x + (seg.first ? 0 : 1)) * nr * (D + 4);
-                    } else {
-                        nr = seg.prefix ? p.rp : p.rs;
-                        slot = (seg.prefix ? p.whole_p : p.whole_s) + (size_t)seg.id * nr * (D + 4);
-                    }
+                    float *slot = part_of<D>(p, seg, nr);
                     part = slot + (size_t)rr * D;
                     if (valid_row && (pair || s == 0))
                         *reinterpret_cast<float2 *>(slot + (size_t)nr * D + rr * 2) = make_float2(R, l);
@@ -1364,12 +1371,49 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
 
 namespace {
 
+// ---- an e4m3 prefix in bf16 ----------------------------------------------------------------
+// A code times its power-of-two scale is exact in bf16, so many rows' products over a shared prefix can
+// run on bf16 copies: 16 instead of 20 matrix instructions a tile, no split of Q and P, and the copy is
+// read and written once where each tile is used by every 256 rows.
+__global__ void __launch_bounds__(256) sv_prefix_values_kernel(const uint4 *k, const uint4 *v, const uint8_t *ks, const uint8_t *vs, uint4 *ko,
+                                                               uint4 *vo, int chunks, int per)
+{
+    grid_dependency_wait();
+    const int c = blockIdx.x * 256 + threadIdx.x;  // 16 codes, `per` chunks to a scale
+    if (c >= chunks)
+        return;
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        const uint4 x = __ldg((which ? v : k) + c);
+        const uint32_t sb = __ldg((which ? vs : ks) + c / per);
+        const float f = sb ? __uint_as_float(sb << 23) : __uint_as_float(0x00400000u);
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        uint32_t o[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[j >> 1] >> (16 * (j & 1))), __NV_E4M3);
+            const float2 t = __half22float2(__half2(h));
+            o[j] = pack_bf16(t.x * f, t.y * f);
+        }
+        uint4 *dst = (which ? vo : ko) + 2 * c;
+        dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    }
+}
+
 // ---- joining the parts of cut rows -----------------------------------------------------
 
 // W warps per row (W = 8: a row's parts are dealt to the warps).  With a prefix
 // every row has parts to join, and the grid goes over the rows; without one only
 // the segments that a stretch's end cuts do, and the grid's x goes over those ends.
-template <int D, int W, bool PREFIX> __global__ void __launch_bounds__(256) sv_attention_join_kernel(AttnParams p, int grid)
+// px: the line that the prefix segments are on, when it is not the sequences'.
+struct PrefixLine {
+    int U, C;             // 0: the same line
+    const float *pieces;
+};
+
+template <int D, int W, bool PREFIX>
+__global__ void __launch_bounds__(256) sv_attention_join_kernel(AttnParams p, int grid, PrefixLine px)
 {
     constexpr int E = D / 32;  // columns of a lane
     __shared__ float sh[W == 1 ? 1 : W * (D + 2)];
@@ -1410,11 +1454,13 @@ template <int D, int W, bool PREFIX> __global__ void __launch_bounds__(256) sv_a
     }
     const int s0 = owner(ut, U, C), s1 = owner(ut + nt - 1, U, C);
     int id_p = 0, up = 0, p0 = 0, p1 = -1;
+    const int Up = px.U ? px.U : U, Cp = px.U ? px.C : C;
+    const float *pieces_p = px.U ? px.pieces : p.pieces;
     if constexpr (PREFIX) {
         id_p = h * p.nbp + R / (2 * kTile);
-        up = id_p * (p.ntp + p.seg_cost);
-        p0 = owner(up + p.seg_cost, U, C);
-        p1 = owner(up + p.seg_cost + p.ntp - 1, U, C);
+        up = id_p * (p.ntp + p.prefix_cost);
+        p0 = owner(up + p.prefix_cost, Up, Cp);
+        p1 = owner(up + p.prefix_cost + p.ntp - 1, Up, Cp);
     }
     const int np = p1 - p0 + 1, n = np + (s1 - s0 + 1);
     // part i: its row of O, and (R, l)
@@ -1428,7 +1474,7 @@ template <int D, int W, bool PREFIX> __global__ void __launch_bounds__(256) sv_a
                 slot = p.whole_p + (size_t)id_p * nr * (D + 4);
             } else {
                 nr = p.rm;
-                slot = p.pieces + (size_t)(2 * (p0 + i) + (stretch(p0 + i, U, C) >= up ? 0 : 1)) * nr * (D + 4);
+                slot = pieces_p + (size_t)(2 * (p0 + i) + (stretch(p0 + i, Up, Cp) >= up ? 0 : 1)) * nr * (D + 4);
             }
         } else {
             rr = rb_row;
@@ -1556,9 +1602,10 @@ sv_status check(const sv_attention_args *a)
 
 // Sizes of a call, false when they pass the 32-bit counts of the kernels.
 struct Plan {
-    int G, nbp, ntp, nbs, rp, rs, rm, seg_cost;
+    int G, nbp, ntp, nbs, rp, rs, rm, seg_cost, prefix_cost;
+    bool split;        // an e4m3 prefix for many rows: in bf16, on a line and in a launch of its own
     int64_t UP, most;  // prefix units, units at full lengths
-    int64_t off_cut, off_wp, off_ws, off_pc, bytes;
+    int64_t off_cut, off_wp, off_ws, off_pc, off_pp, off_pv, bytes;
 };
 
 bool plan(const sv_attention_args &a, Plan &w)
@@ -1567,15 +1614,19 @@ bool plan(const sv_attention_args &a, Plan &w)
     if (a.heads_q > big / 4 || a.max_len > big - 256 || a.prefix_len > big - 256 || a.B > big / a.T / a.heads_q)
         return false;
     w.G = (int)(a.heads_q / a.heads_kv);
-    // A segment's start and end (queries, epilogue) against a tile, so that short segments and long ones fill the
-    // stretches alike.  Measured: 256 chains of 8 over up to 2048 keys 124, 116, 114 us with 1, 2, 3; of 6 over 4096 e4m3
-    // keys 282, 261, 253, 248 us with 1, 3, 4, 6; with a prefix (long segments, all alike) 1 is best, 108 against 111 us.
-    w.seg_cost = a.format == SV_KV_E4M3 && a.prefix_len == 0 && a.T * w.G <= kNarrowMost ? 6 : a.prefix_len == 0 ? 3 : 1;
     const int64_t rows = a.B * a.T * w.G, seq_rows = a.T * w.G;
     w.ntp = (int)((a.prefix_len + kTile - 1) / kTile);
     w.nbp = (int)((rows + 2 * kTile - 1) / (2 * kTile));
     w.nbs = (int)((seq_rows + 2 * kTile - 1) / (2 * kTile));
-    w.UP = a.prefix_len > 0 ? a.heads_kv * w.nbp * (w.ntp + w.seg_cost) : 0;  // below 2^31 * 2^24
+    // A segment's start and end (queries, epilogue) against a tile, so that short segments and long ones fill the
+    // stretches alike.  Measured: 256 chains of 8 over up to 2048 keys 124, 116, 114 us with 1, 2, 3; of 6 over 4096 e4m3
+    // keys 282, 261, 253, 248 us with 1, 3, 4, 6; with a prefix (long segments, all alike) 1 is best, 108 against 111 us.
+    w.split = a.format == SV_KV_E4M3 && a.prefix_len > 0 && w.nbp >= 2;
+    w.seg_cost = a.prefix_len > 0 && !w.split ? 1 : a.format == SV_KV_E4M3 && seq_rows <= kNarrowMost ? 6 : 3;
+    w.prefix_cost = 1;
+    w.UP = a.prefix_len > 0 ? a.heads_kv * w.nbp * (w.ntp + w.prefix_cost) : 0;  // below 2^31 * 2^24
+    if (a.prefix_len > big / (a.heads_kv * a.head_dim))
+        return false;
     const int64_t tiles = (a.max_len + kTile - 1) / kTile + 1 + w.seg_cost;
     if (w.UP > big / 2 || a.heads_kv * w.nbs > big || a.B * a.heads_kv * w.nbs > big || tiles > big / 2 / (a.B * a.heads_kv * w.nbs + 1))
         return false;
@@ -1595,6 +1646,12 @@ bool plan(const sv_attention_args &a, Plan &w)
     at = (at + 1023) / 1024 * 1024;
     w.off_pc = at;
     at += (int64_t)2 * kMaxCtas * w.rm * per;
+    at = (at + 1023) / 1024 * 1024;
+    w.off_pp = at;
+    at += w.split ? (int64_t)2 * kMaxCtas * w.rp * per : 0;
+    at = (at + 1023) / 1024 * 1024;
+    w.off_pv = at;  // K, then V, of the prefix in bf16
+    at += w.split ? 4 * a.prefix_len * a.heads_kv * a.head_dim : 0;
     w.bytes = at;
     return true;
 }
@@ -1640,52 +1697,50 @@ int device_sms()
     return n;
 }
 
-template <int D, bool E4> sv_status launch(const Maps &maps, const AttnParams &p, int C, cudaStream_t st)
+cudaLaunchConfig_t config(unsigned x, unsigned y, int threads, size_t smem, cudaStream_t st, cudaLaunchAttribute *attr)
 {
-    cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)C);
+    cfg.gridDim = dim3(x, y);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t e;
-    // 8-bit caches, few rows and no prefix: the products turned around (attention_narrow.cuh)
+    return cfg;
+}
+
+template <int D, bool E4> cudaError_t launch_rows(const Maps &maps, const AttnParams &p, int C, cudaStream_t st)
+{
+    cudaLaunchAttribute attr[1];
     const int rows = p.T * p.G;
+    // 8-bit caches and few rows: the products turned around (attention_narrow.cuh)
     if (E4 && p.UP == 0 && rows <= kNarrowMost) {
-        cfg.blockDim = dim3(kNarrowThreads);
-        cfg.dynamicSmemBytes = narrow_smem<D>();
-        e = rows <= 16   ? cudaLaunchKernelEx(&cfg, sv_attention_narrow_kernel<D, 8>, maps, p)
-            : rows <= 32 ? cudaLaunchKernelEx(&cfg, sv_attention_narrow_kernel<D, 16>, maps, p)
-                         : cudaLaunchKernelEx(&cfg, sv_attention_narrow_kernel<D, 24>, maps, p);
-    } else {
-        cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = smem_bytes<D, E4>();
-        e = cudaLaunchKernelEx(&cfg, sv_attention_kernel<D, E4>, maps, p);
+        const cudaLaunchConfig_t cfg = config((unsigned)C, 1, kNarrowThreads, narrow_smem<D>(), st, attr);
+        return rows <= 16   ? cudaLaunchKernelEx(&cfg, sv_attention_narrow_kernel<D, 8>, maps, p)
+               : rows <= 32 ? cudaLaunchKernelEx(&cfg, sv_attention_narrow_kernel<D, 16>, maps, p)
+                            : cudaLaunchKernelEx(&cfg, sv_attention_narrow_kernel<D, 24>, maps, p);
     }
-    if (e == cudaSuccess) {
-        // few rows: a CTA joins one row, its parts dealt to the warps
-        const long long all = (long long)p.B * p.T * p.Hq;
-        cfg.blockDim = dim3(256);
-        cfg.dynamicSmemBytes = 0;
-        if (p.UP > 0) {
-            const bool wide = all <= 1024;
-            cfg.gridDim = dim3((unsigned)(wide ? all : (all + 7) / 8));
-            e = wide ? cudaLaunchKernelEx(&cfg, sv_attention_join_kernel<D, 8, true>, p, C)
-                     : cudaLaunchKernelEx(&cfg, sv_attention_join_kernel<D, 1, true>, p, C);
-        } else {
-            const bool wide = p.rs <= 32;
-            cfg.gridDim = dim3((unsigned)C, (unsigned)(wide ? p.rs : (p.rs + 7) / 8));
-            e = wide ? cudaLaunchKernelEx(&cfg, sv_attention_join_kernel<D, 8, false>, p, C)
-                     : cudaLaunchKernelEx(&cfg, sv_attention_join_kernel<D, 1, false>, p, C);
-        }
+    const cudaLaunchConfig_t cfg = config((unsigned)C, 1, kThreads, smem_bytes<D, E4>(), st, attr);
+    return cudaLaunchKernelEx(&cfg, sv_attention_kernel<D, E4>, maps, p);
+}
+
+template <int D> cudaError_t launch_join(const AttnParams &p, int C, const PrefixLine &px, cudaStream_t st)
+{
+    cudaLaunchAttribute attr[1];
+    const long long all = (long long)p.B * p.T * p.Hq;
+    // few rows: a CTA joins one row, its parts dealt to the warps
+    if (p.join_all) {
+        const bool wide = all <= 1024;
+        const cudaLaunchConfig_t cfg = config((unsigned)(wide ? all : (all + 7) / 8), 1, 256, 0, st, attr);
+        return wide ? cudaLaunchKernelEx(&cfg, sv_attention_join_kernel<D, 8, true>, p, C, px)
+                    : cudaLaunchKernelEx(&cfg, sv_attention_join_kernel<D, 1, true>, p, C, px);
     }
-    if (e != cudaSuccess) {
-        cudaGetLastError();
-        return SV_ERR_CUDA;
-    }
-    return SV_OK;
+    const bool wide = p.rs <= 32;
+    const cudaLaunchConfig_t cfg = config((unsigned)C, (unsigned)(wide ? p.rs : (p.rs + 7) / 8), 256, 0, st, attr);
+    return wide ? cudaLaunchKernelEx(&cfg, sv_attention_join_kernel<D, 8, false>, p, C, px)
+                : cudaLaunchKernelEx(&cfg, sv_attention_join_kernel<D, 1, false>, p, C, px);
 }
 
 } // namespace
@@ -1754,15 +1809,23 @@ extern "C" sv_status spec_verify_attention(const sv_attention_args *args, void *
         map(&maps.kn, a.k_new, false, a.B, a.T, sb, sn);
         map(&maps.vn, a.v_new, false, a.B, a.T, sb, sn);
     }
+    p.nb = (int)a.B;
+    p.join_all = a.prefix_len > 0;
     p.seg_cost = w.seg_cost;
+    p.prefix_cost = w.prefix_cost;
     p.tma_q = a.T * w.G <= kTile;
     if (p.tma_q) {  // box: one token range's rows of one head, 64 wide
         const int64_t st_ = a.T > 1 ? a.q_stride_t : qrow, sb_ = a.B > 1 ? a.q_stride_b : a.T * st_;
         ok = ok && make_map(&maps.q, a.q, false, a.B, a.T, a.heads_q, D, sb_, st_, (int)a.T, w.G);
     }
-    if (a.prefix_len > 0) {
-        map(&maps.kp, a.k_prefix, e4, 1, a.prefix_len, a.prefix_len * nrow, nrow);
-        map(&maps.vp, a.v_prefix, e4, 1, a.prefix_len, a.prefix_len * nrow, nrow);
+    unsigned char *ws = static_cast<unsigned char *>(a.workspace);
+    const int64_t prefix_values = a.prefix_len * nrow;
+    if (w.split) {
+        map(&maps.kp, ws + w.off_pv, false, 1, a.prefix_len, prefix_values, nrow);
+        map(&maps.vp, ws + w.off_pv + 2 * prefix_values, false, 1, a.prefix_len, prefix_values, nrow);
+    } else if (a.prefix_len > 0) {
+        map(&maps.kp, a.k_prefix, e4, 1, a.prefix_len, prefix_values, nrow);
+        map(&maps.vp, a.v_prefix, e4, 1, a.prefix_len, prefix_values, nrow);
     }
     if (!ok)
         return SV_ERR_CUDA;
@@ -1777,7 +1840,6 @@ extern "C" sv_status spec_verify_attention(const sv_attention_args *args, void *
     p.out = static_cast<__nv_bfloat16 *>(a.out);
     p.lse = a.lse;
     p.status = a.status;
-    unsigned char *ws = static_cast<unsigned char *>(a.workspace);
     p.seg_start = reinterpret_cast<int32_t *>(ws);
     p.cuts = reinterpret_cast<int4 *>(ws + w.off_cut);
     p.whole_p = reinterpret_cast<float *>(ws + w.off_wp);
@@ -1801,11 +1863,38 @@ extern "C" sv_status spec_verify_attention(const sv_attention_args *args, void *
     p.rs = w.rs;
     p.rm = w.rm;
     p.c = (float)(a.softmax_scale * 1.4426950408889634);
-    int C = sms < kMaxCtas ? sms : kMaxCtas;
-    if (w.most < C)
-        C = (int)w.most;
+    const int most = sms < kMaxCtas ? sms : kMaxCtas;
+    auto ctas = [&](int64_t units) { return units < most ? (int)units : most; };
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (D == 64)
-        return e4 ? launch<64, true>(maps, p, C, s) : launch<64, false>(maps, p, C, s);
-    return e4 ? launch<128, true>(maps, p, C, s) : launch<128, false>(maps, p, C, s);
+    cudaError_t e = cudaSuccess;
+    PrefixLine px = {0, 0, nullptr};
+    if (w.split) {
+        cudaLaunchAttribute attr[1];
+        const int chunks = (int)(prefix_values / 16);
+        const cudaLaunchConfig_t cfg = config((unsigned)((chunks + 255) / 256), 1, 256, 0, s, attr);
+        e = cudaLaunchKernelEx(&cfg, sv_prefix_values_kernel, static_cast<const uint4 *>(a.k_prefix),
+                               static_cast<const uint4 *>(a.v_prefix), a.k_prefix_scale, a.v_prefix_scale,
+                               reinterpret_cast<uint4 *>(ws + w.off_pv), reinterpret_cast<uint4 *>(ws + w.off_pv + 2 * prefix_values),
+                               chunks, D / 16);
+        AttnParams pp = p;
+        pp.nb = 0;
+        pp.seg_cost = w.prefix_cost;
+        pp.rm = w.rp;
+        pp.pieces = reinterpret_cast<float *>(ws + w.off_pp);
+        px = {(int)w.UP, ctas(w.UP), pp.pieces};
+        if (e == cudaSuccess)
+            e = D == 64 ? launch_rows<64, false>(maps, pp, px.C, s) : launch_rows<128, false>(maps, pp, px.C, s);
+        p.UP = 0;
+    }
+    const int C = ctas(w.split ? w.most - w.UP : w.most);
+    if (e == cudaSuccess)
+        e = D == 64 ? (e4 ? launch_rows<64, true>(maps, p, C, s) : launch_rows<64, false>(maps, p, C, s))
+                    : (e4 ? launch_rows<128, true>(maps, p, C, s) : launch_rows<128, false>(maps, p, C, s));
+    if (e == cudaSuccess)
+        e = D == 64 ? launch_join<64>(p, C, px, s) : launch_join<128>(p, C, px, s);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return SV_ERR_CUDA;
+    }
+    return SV_OK;
 }

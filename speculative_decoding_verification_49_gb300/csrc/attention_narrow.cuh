@@ -655,8 +655,9 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) sv_attention_narrow_kernel(
             }
             bar_sync(6 + group, 256);  // every slot's product and sums are complete
             tc_fence_after();
-            const bool direct = seg.whole();
-            float *piece = p.pieces + (size_t)(2 * blockIdx.x + (seg.first ? 0 : 1)) * p.rm * (D + 4);
+            const bool direct = !p.join_all && seg.whole();
+            int prow;
+            float *piece = part_of<D>(p, seg, prow);
             if (slot == 0 && pt < nrow) {
                 const int r = lo + pt;
                 const float ma = ctl.mu[0][r], mb = ctl.mu[1][r], mn = fmax_nan(ma, mb);
@@ -672,7 +673,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) sv_attention_narrow_kernel(
                         p.lse[(size_t)tok * p.Hq + seg.h * p.G + (Rg - tok * p.G)] = l == 0.0f ? -INFINITY : (R + log2f(l)) * 0.69314718055994531f;
                     }
                 } else {
-                    *reinterpret_cast<float2 *>(piece + (size_t)p.rm * D + r * 2) = make_float2(R, l);
+                    *reinterpret_cast<float2 *>(piece + (size_t)prow * D + r * 2) = make_float2(R, l);
                 }
                 ctl.fac[0][r] = l != l ? l : fa;  // NaN reaches every column
                 ctl.fac[1][r] = fb;

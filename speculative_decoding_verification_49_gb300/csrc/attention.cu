@@ -82,6 +82,7 @@ constexpr int kThreads = 384;          // warp 11 idles: registers are moved by 
 // other 128 keep 72: the same 64512 in all
 constexpr int kRegsStart = 168, kRegsSoftmax = 216, kRegsOther = 72;
 static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * kRegsStart, "the split is covered by what the launch holds");
+constexpr int kSoloSegments = 152, kSoloTiles = 10;  // a CTA each for segments of at most so many tiles
 constexpr int kMaxCtas = 160;         // of the grid; the workspace counts on it
 constexpr uint32_t kTmemCols = 512;
 constexpr uint64_t kWaitNs = 2000000000ull;
@@ -111,6 +112,7 @@ struct AttnParams {
     int B, T, Hq, H, G, L, Lp;
     int has_new, max_len;
     int nb;                 // sequences on the line: B, or none (the prefix alone)
+    int solo;               // a CTA for each segment: nothing is cut
     int join_all;           // every row has parts elsewhere: nothing is written directly
     int seg_cost;           // what a segment counts beside its tiles, in tiles
     int prefix_cost;        // the same of the line that the prefix segments are on (for the joining kernel)
@@ -482,6 +484,20 @@ __device__ __forceinline__ float pow2i(int e)
 template <int kThr, class Ct> __device__ __forceinline__ void find_stretch(const AttnParams &p, Ct &ctl, int &u0, int &u1)
 {
     // ---- units of every sequence: this CTA's stretch and where it starts ----
+    if (p.solo) {
+        const int per = p.H * p.nbs, b = blockIdx.x / per;
+        const int units = p.seg_cost + tiles_of(p, clean_len(p, raw_len(p, b)).n);
+        u0 = (blockIdx.x - b * per) * units;
+        u1 = u0 + units;
+        if (threadIdx.x == 0) {
+            ctl.start_b = b;
+            ctl.start_ub = 0;
+        }
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        return;
+    }
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int per = p.H * p.nbs;  // segments of a sequence
     const int chunk = cdiv(p.nb, kThr);
@@ -561,7 +577,7 @@ __device__ __forceinline__ void produce(const AttnParams &p, const Maps &maps, C
     };
     while (ok) {
         const bool more = walk.next(p, seg);
-        if (!cut_known && !p.join_all) {
+        if (!cut_known && !p.join_all && !p.solo) {
             // the segment that this CTA's stretch starts inside of, for the joining kernel: the stretch starts at its tile t0
             const bool cut = more && seg.t0 > 0;
             p.cuts[2 * blockIdx.x] = make_int4(cut ? seg.row0 : -1, cut ? seg.nrows : 0, cut ? walk.u0 - seg.t0 : 0, cut ? seg.nt : 0);
@@ -1403,142 +1419,217 @@ __global__ void __launch_bounds__(256) sv_prefix_values_kernel(const uint4 *k, c
 
 // ---- joining the parts of cut rows -----------------------------------------------------
 
-// W warps per row (W = 8: a row's parts are dealt to the warps).  With a prefix
-// every row has parts to join, and the grid goes over the rows; without one only
-// the segments that a stretch's end cuts do, and the grid's x goes over those ends.
 // px: the line that the prefix segments are on, when it is not the sequences'.
 struct PrefixLine {
     int U, C;             // 0: the same line
     const float *pieces;
 };
 
-template <int D, int W, bool PREFIX>
-__global__ void __launch_bounds__(256) sv_attention_join_kernel(AttnParams p, int grid, PrefixLine px)
+// A segment's parts: CTAs c0 .. c0 + n - 1 of its line, or the segment whole.
+struct Parts {
+    const float *whole, *pieces;  // slots
+    int rows, wrows;              // rows of a slot
+    int c0, n, tail;              // tail: the first part is the last of its CTA's stretch, not the first
+
+    // The segment's units are us .., its nt tiles those from t0 on, in a line of U units cut for C CTAs.  Of the CTAs
+    // only the first can have begun with another segment.
+    __device__ __forceinline__ void find(int us, int t0, int nt, int U, int C)
+    {
+        c0 = owner(t0, U, C);
+        n = owner(t0 + nt - 1, U, C) - c0 + 1;
+        tail = stretch(c0, U, C) < us;
+    }
+
+    template <int D> __device__ __forceinline__ const float *at(int i, int rr, float2 &ml) const
+    {
+        const bool one = n == 1;
+        const int nr = one ? wrows : rows;
+        const float *slot = one ? whole : pieces + (size_t)(2 * (c0 + i) + (i == 0 ? tail : 0)) * nr * (D + 4);
+        ml = __ldg(reinterpret_cast<const float2 *>(slot + (size_t)nr * D + rr * 2));
+        return slot + (size_t)rr * D;
+    }
+};
+
+template <int D> struct Joined {
+    static constexpr int E = D / 32;  // columns of a lane
+    float top, l, acc[E];
+
+    __device__ __forceinline__ void start()
+    {
+        top = -INFINITY;
+        l = 0.0f;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            acc[e] = 0.0f;
+    }
+
+    __device__ __forceinline__ static void load(const float *o, int lane, float *v)
+    {
+        if constexpr (E == 4) {
+            const float4 x = __ldg(reinterpret_cast<const float4 *>(o) + lane);
+            v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+        } else {
+            const float2 x = __ldg(reinterpret_cast<const float2 *>(o) + lane);
+            v[0] = x.x, v[1] = x.y;
+        }
+    }
+
+    // Takes part (R, l) = ml with values v in.
+    __device__ __forceinline__ void add(float2 ml, const float *v)
+    {
+        const float mn = fmaxf(top, ml.x);
+        const float fo = top == -INFINITY ? 0.0f : ex2(top - mn), fn = ml.x == -INFINITY ? 0.0f : ex2(ml.x - mn);
+        l = (l != l ? l : l * fo) + (ml.y != ml.y ? ml.y : ml.y * fn);
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            acc[e] = acc[e] * fo + (fn == 0.0f ? 0.0f : fn * v[e]);
+        top = mn;
+    }
+
+    __device__ __forceinline__ void write(const AttnParams &p, long long row, int lane) const
+    {
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        __nv_bfloat16 *dst = p.out + row * D + lane * E;
+        if constexpr (E == 4)
+            *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
+        else
+            *reinterpret_cast<unsigned *>(dst) = pack_bf16(acc[0] * inv, acc[1] * inv);
+        if (p.lse && lane == 0)
+            p.lse[row] = l == 0.0f ? -INFINITY : (top + log2f(l)) * 0.69314718055994531f;
+    }
+};
+
+// With a prefix every row has parts to join.  Grid: x = (sequence, head), y = 32 of its rows, 4 to a warp.  The
+// 64-bit divisions behind a segment's CTAs are done once for the 4, those of the segments in lanes side by side;
+// the 4 rows' loads are in flight together.
+template <int D> __global__ void __launch_bounds__(256, 3) sv_attention_join_kernel(AttnParams p, int grid, PrefixLine px)
 {
-    constexpr int E = D / 32;  // columns of a lane
+    constexpr int kR = 4;
+    grid_dependency_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int b = blockIdx.x / p.H, h = blockIdx.x - b * p.H, nrows = p.T * p.G;
+    const int local = blockIdx.y * (8 * kR) + warp * kR;
+    if (local >= nrows)
+        return;
+    const int U = __ldg(&p.seg_start[p.B]), ub = __ldg(&p.seg_start[b]), ue = __ldg(&p.seg_start[b + 1]);
+    const int nt = (ue - ub) / (p.H * p.nbs) - p.seg_cost, C = min(grid, U);
+    const int rb = local / (2 * kTile), id_s = (b * p.H + h) * p.nbs + rb;
+    // the 4 rows lie in one or two blocks of the prefix's segments
+    const int R0 = b * nrows + local, block0 = R0 / (2 * kTile), last = min(kR, nrows - local) - 1;
+    // lane 0: the sequence's own segment, lanes 1 and 2: the prefix's
+    const int k = min(lane, 2), id_p = h * p.nbp + min(block0 + max(k - 1, 0), p.nbp - 1);
+    Parts q;
+    {
+        const int cost = k ? p.prefix_cost : p.seg_cost;
+        const int us = k ? id_p * (p.ntp + cost) : ub + (h * p.nbs + rb) * (nt + cost);
+        q.find(us, us + cost, k ? p.ntp : nt, k && px.U ? px.U : U, k && px.U ? px.C : C);
+    }
+    Joined<D> j[kR];
+#pragma unroll
+    for (int r = 0; r < kR; ++r)
+        j[r].start();
+    // the sources in turn; rows that are not of this one take its part as one without keys
+#pragma unroll 1
+    for (int src = 0; src < 3; ++src) {
+        if (src == 2 && (R0 + last) / (2 * kTile) == block0)
+            break;
+        const int id = h * p.nbp + block0 + src - 1;
+        Parts t;
+        t.c0 = __shfl_sync(0xffffffffu, q.c0, src);
+        t.n = __shfl_sync(0xffffffffu, q.n, src);
+        t.tail = __shfl_sync(0xffffffffu, q.tail, src);
+        t.whole = src ? p.whole_p + (size_t)id * p.rp * (D + 4) : p.whole_s + (size_t)id_s * p.rs * (D + 4);
+        t.wrows = src ? p.rp : p.rs;
+        t.pieces = src && px.U ? px.pieces : p.pieces;
+        t.rows = p.rm;
+#pragma unroll 1
+        for (int i = 0; i < t.n; ++i) {
+            float2 ml[kR];
+            float v[kR][Joined<D>::E];
+#pragma unroll
+            for (int r = 0; r < kR; ++r) {
+                const int row = min(r, last);
+                j[r].load(t.at<D>(i, (src ? R0 + row : local + row) % (2 * kTile), ml[r]), lane, v[r]);
+                if (src && (R0 + row) / (2 * kTile) - block0 != src - 1)
+                    ml[r] = make_float2(-INFINITY, 0.0f);
+            }
+#pragma unroll
+            for (int r = 0; r < kR; ++r)
+                j[r].add(ml[r], v[r]);
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < kR; ++r)
+        if (r <= last) {
+            const int tok = (local + r) / p.G;
+            j[r].write(p, ((long long)b * p.T + tok) * p.Hq + h * p.G + (local + r - tok * p.G), lane);
+        }
+}
+
+// Without a prefix only the segments that a stretch's end cuts have parts.  Grid: x = those ends, y = rows; W
+// warps per row (W = 8: few rows with many parts, which are dealt to the warps).
+template <int D, int W> __global__ void __launch_bounds__(256) sv_attention_join_cut_kernel(AttnParams p, int grid)
+{
+    constexpr int E = D / 32;
     __shared__ float sh[W == 1 ? 1 : W * (D + 2)];
     grid_dependency_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int U = __ldg(&p.seg_start[p.B]);
-    const int C = min(grid, U);
-    long long row;
-    int R, local, rb_row, us, ut, nt, id_s = 0, h;
-    if constexpr (PREFIX) {
-        row = W == 1 ? (long long)blockIdx.x * 8 + warp : blockIdx.x;
-        if (row >= (long long)p.B * p.T * p.Hq)
-            return;
-        const int hq = (int)(row % p.Hq), tok = (int)(row / p.Hq), b = tok / p.T;
-        h = hq / p.G;
-        R = tok * p.G + (hq - h * p.G);
-        local = R - b * p.T * p.G;
-        const int ub = __ldg(&p.seg_start[b]), ue = __ldg(&p.seg_start[b + 1]);
-        nt = (ue - ub) / (p.H * p.nbs) - p.seg_cost;
-        const int rb = local / (2 * kTile);
-        id_s = (b * p.H + h) * p.nbs + rb;
-        us = ub + (h * p.nbs + rb) * (nt + p.seg_cost);
-        ut = us + p.seg_cost;  // its first tile's unit
-        rb_row = local % (2 * kTile);
-    } else {
-        const int4 cut = __ldg(&p.cuts[2 * blockIdx.x]);
-        rb_row = W == 1 ? (int)blockIdx.y * 8 + warp : (int)blockIdx.y;
-        ut = cut.z;
-        nt = cut.w;
-        // one end of those that cut this segment does the work: the first
-        if (cut.x < 0 || rb_row >= cut.y || owner(ut, U, C) != (int)blockIdx.x - 1)
-            return;
-        h = __ldg(&p.cuts[2 * blockIdx.x + 1]).x;
-        us = ut - p.seg_cost;
-        R = cut.x + rb_row;
-        const int tok = R / p.G;
-        row = (long long)tok * p.Hq + h * p.G + (R - tok * p.G);
-    }
-    const int s0 = owner(ut, U, C), s1 = owner(ut + nt - 1, U, C);
-    int id_p = 0, up = 0, p0 = 0, p1 = -1;
-    const int Up = px.U ? px.U : U, Cp = px.U ? px.C : C;
-    const float *pieces_p = px.U ? px.pieces : p.pieces;
-    if constexpr (PREFIX) {
-        id_p = h * p.nbp + R / (2 * kTile);
-        up = id_p * (p.ntp + p.prefix_cost);
-        p0 = owner(up + p.prefix_cost, Up, Cp);
-        p1 = owner(up + p.prefix_cost + p.ntp - 1, Up, Cp);
-    }
-    const int np = p1 - p0 + 1, n = np + (s1 - s0 + 1);
-    // part i: its row of O, and (R, l)
-    auto part = [&](int i, const float *&o) {
-        const float *slot;
-        int nr, rr;
-        if (i < np) {
-            rr = R % (2 * kTile);
-            if (np == 1) {
-                nr = p.rp;
-                slot = p.whole_p + (size_t)id_p * nr * (D + 4);
-            } else {
-                nr = p.rm;
-                slot = pieces_p + (size_t)(2 * (p0 + i) + (stretch(p0 + i, Up, Cp) >= up ? 0 : 1)) * nr * (D + 4);
-            }
-        } else {
-            rr = rb_row;
-            if (s0 == s1) {
-                nr = p.rs;
-                slot = p.whole_s + (size_t)id_s * nr * (D + 4);
-            } else {
-                const int c = s0 + i - np;
-                nr = p.rm;
-                slot = p.pieces + (size_t)(2 * c + (stretch(c, U, C) >= us ? 0 : 1)) * nr * (D + 4);
-            }
-        }
-        o = slot + (size_t)rr * D;
-        return *reinterpret_cast<const float2 *>(slot + (size_t)nr * D + rr * 2);
-    };
-    const float *op;
-    float top = -INFINITY;
-    for (int i = lane; i < n; i += 32)
-        top = fmaxf(top, part(i, op).x);
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1)
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    float acc[E], l = 0.0f;
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-        acc[e] = 0.0f;
-#pragma unroll 4
-    for (int i = W == 1 ? 0 : warp; i < n; i += W) {
-        const float2 m = part(i, op);
-        const float f = m.x == -INFINITY ? 0.0f : ex2(m.x - top);
-        l += m.y != m.y ? m.y : f * m.y;
-        alignas(16) float o[E];
-        if constexpr (E == 4)
-            *reinterpret_cast<float4 *>(o) = *reinterpret_cast<const float4 *>(op + lane * 4);
-        else
-            *reinterpret_cast<float2 *>(o) = *reinterpret_cast<const float2 *>(op + lane * 2);
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            acc[e] += f == 0.0f ? 0.0f : f * o[e];
+    const int4 cut = __ldg(&p.cuts[2 * blockIdx.x]);
+    const int U = __ldg(&p.seg_start[p.B]), h = __ldg(&p.cuts[2 * blockIdx.x + 1]).x;
+    const int rr = W == 1 ? (int)blockIdx.y * 8 + warp : (int)blockIdx.y;
+    if (cut.x < 0 || rr >= cut.y)
+        return;
+    Parts sp;
+    sp.find(cut.z - p.seg_cost, cut.z, cut.w, U, min(grid, U));
+    // one end of those that cut this segment does the work: the first
+    if (sp.c0 != (int)blockIdx.x - 1)
+        return;
+    sp.whole = nullptr;  // there are two parts or more
+    sp.wrows = 0;
+    sp.pieces = p.pieces;
+    sp.rows = p.rm;
+    Joined<D> j;
+    j.start();
+    float2 ml;
+#pragma unroll 2
+    for (int i = W == 1 ? 0 : warp; i < sp.n; i += W) {
+        float v[E];
+        j.load(sp.at<D>(i, rr, ml), lane, v);
+        j.add(ml, v);
     }
     if constexpr (W > 1) {
 #pragma unroll
         for (int e = 0; e < E; ++e)
-            sh[warp * (D + 2) + lane * E + e] = acc[e];
-        if (lane == 0)
-            sh[warp * (D + 2) + D] = l;
+            sh[warp * (D + 2) + lane * E + e] = j.acc[e];
+        if (lane == 0) {
+            sh[warp * (D + 2) + D] = j.top;
+            sh[warp * (D + 2) + D + 1] = j.l;
+        }
         __syncthreads();
         if (warp != 0)
             return;
-        for (int w = 1; w < W; ++w) {
-            l += sh[w * (D + 2) + D];
+        float top = -INFINITY, l = 0.0f, acc[E];
+        for (int w = 0; w < W; ++w)
+            top = fmaxf(top, sh[w * (D + 2) + D]);
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            acc[e] = 0.0f;
+        for (int w = 0; w < W; ++w) {
+            const float m = sh[w * (D + 2) + D], y = sh[w * (D + 2) + D + 1];
+            const float f = m == -INFINITY ? 0.0f : ex2(m - top);
+            l += y != y ? y : f * y;
 #pragma unroll
             for (int e = 0; e < E; ++e)
-                acc[e] += sh[w * (D + 2) + lane * E + e];
+                acc[e] += f == 0.0f ? 0.0f : f * sh[w * (D + 2) + lane * E + e];
         }
+        j.top = top;
+        j.l = l;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            j.acc[e] = acc[e];
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    __nv_bfloat16 *dst = p.out + row * D + lane * E;
-    if constexpr (E == 4)
-        *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
-    else
-        *reinterpret_cast<unsigned *>(dst) = pack_bf16(acc[0] * inv, acc[1] * inv);
-    if (p.lse && lane == 0)
-        p.lse[row] = l == 0.0f ? -INFINITY : (top + log2f(l)) * 0.69314718055994531f;
+    const int R = cut.x + rr, tok = R / p.G;
+    j.write(p, (long long)tok * p.Hq + h * p.G + (R - tok * p.G), lane);
 }
 
 // ---- host side -------------------------------------------------------------------------
@@ -1603,6 +1694,7 @@ sv_status check(const sv_attention_args *a)
 // Sizes of a call, false when they pass the 32-bit counts of the kernels.
 struct Plan {
     int G, nbp, ntp, nbs, rp, rs, rm, seg_cost, prefix_cost;
+    bool solo;         // few short segments: a CTA each, in one launch
     bool split;        // an e4m3 prefix for many rows: in bf16, on a line and in a launch of its own
     int64_t UP, most;  // prefix units, units at full lengths
     int64_t off_cut, off_wp, off_ws, off_pc, off_pp, off_pv, bytes;
@@ -1630,6 +1722,10 @@ bool plan(const sv_attention_args &a, Plan &w)
     const int64_t tiles = (a.max_len + kTile - 1) / kTile + 1 + w.seg_cost;
     if (w.UP > big / 2 || a.heads_kv * w.nbs > big || a.B * a.heads_kv * w.nbs > big || tiles > big / 2 / (a.B * a.heads_kv * w.nbs + 1))
         return false;
+    // Few short segments are not cut: each is one CTA's, and there is nothing to join.  Measured with 9 tiles (one token
+    // over 1024 keys, 2 heads): cut in single tiles and joined by a second launch 13.5 us in a replayed graph and
+    // 23.4 us a call, on one CTA each 12.3 and 19.5.  The longest tile count allowed is where the two meet.
+    w.solo = a.prefix_len == 0 && a.B * a.heads_kv * w.nbs <= kSoloSegments && tiles - w.seg_cost <= kSoloTiles;
     w.most = w.UP + a.B * a.heads_kv * w.nbs * tiles;
     w.rp = (int)(rows < 2 * kTile ? rows : 2 * kTile);
     w.rs = (int)(seq_rows < 2 * kTile ? seq_rows : 2 * kTile);
@@ -1729,18 +1825,14 @@ template <int D, bool E4> cudaError_t launch_rows(const Maps &maps, const AttnPa
 template <int D> cudaError_t launch_join(const AttnParams &p, int C, const PrefixLine &px, cudaStream_t st)
 {
     cudaLaunchAttribute attr[1];
-    const long long all = (long long)p.B * p.T * p.Hq;
-    // few rows: a CTA joins one row, its parts dealt to the warps
     if (p.join_all) {
-        const bool wide = all <= 1024;
-        const cudaLaunchConfig_t cfg = config((unsigned)(wide ? all : (all + 7) / 8), 1, 256, 0, st, attr);
-        return wide ? cudaLaunchKernelEx(&cfg, sv_attention_join_kernel<D, 8, true>, p, C, px)
-                    : cudaLaunchKernelEx(&cfg, sv_attention_join_kernel<D, 1, true>, p, C, px);
+        const cudaLaunchConfig_t cfg = config((unsigned)(p.B * p.H), (unsigned)((p.T * p.G + 31) / 32), 256, 0, st, attr);
+        return cudaLaunchKernelEx(&cfg, sv_attention_join_kernel<D>, p, C, px);
     }
     const bool wide = p.rs <= 32;
     const cudaLaunchConfig_t cfg = config((unsigned)C, (unsigned)(wide ? p.rs : (p.rs + 7) / 8), 256, 0, st, attr);
-    return wide ? cudaLaunchKernelEx(&cfg, sv_attention_join_kernel<D, 8, false>, p, C, px)
-                : cudaLaunchKernelEx(&cfg, sv_attention_join_kernel<D, 1, false>, p, C, px);
+    return wide ? cudaLaunchKernelEx(&cfg, sv_attention_join_cut_kernel<D, 8>, p, C)
+                : cudaLaunchKernelEx(&cfg, sv_attention_join_cut_kernel<D, 1>, p, C);
 }
 
 } // namespace
@@ -1810,6 +1902,7 @@ extern "C" sv_status spec_verify_attention(const sv_attention_args *args, void *
         map(&maps.vn, a.v_new, false, a.B, a.T, sb, sn);
     }
     p.nb = (int)a.B;
+    p.solo = w.solo;
     p.join_all = a.prefix_len > 0;
     p.seg_cost = w.seg_cost;
     p.prefix_cost = w.prefix_cost;
@@ -1886,11 +1979,11 @@ extern "C" sv_status spec_verify_attention(const sv_attention_args *args, void *
             e = D == 64 ? launch_rows<64, false>(maps, pp, px.C, s) : launch_rows<128, false>(maps, pp, px.C, s);
         p.UP = 0;
     }
-    const int C = ctas(w.split ? w.most - w.UP : w.most);
+    const int C = w.solo ? (int)(a.B * a.heads_kv * w.nbs) : ctas(w.split ? w.most - w.UP : w.most);
     if (e == cudaSuccess)
         e = D == 64 ? (e4 ? launch_rows<64, true>(maps, p, C, s) : launch_rows<64, false>(maps, p, C, s))
                     : (e4 ? launch_rows<128, true>(maps, p, C, s) : launch_rows<128, false>(maps, p, C, s));
-    if (e == cudaSuccess)
+    if (e == cudaSuccess && !w.solo)
         e = D == 64 ? launch_join<64>(p, C, px, s) : launch_join<128>(p, C, px, s);
     if (e != cudaSuccess) {
         cudaGetLastError();

@@ -259,6 +259,35 @@ def test_attention_matches_the_reference(B, T, H, G, D, L, prefix, new, tree, fm
 
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
 @pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("T,G", [(4, 4), (17, 1), (5, 5), (31, 1), (8, 4), (11, 3), (5, 8), (6, 8), (7, 7), (21, 3), (8, 8),
+                                 (13, 5), (9, 14), (16, 8), (43, 3), (32, 8), (37, 7)])
+def test_attention_rows_of_a_sequence(T, G, D, fmt):
+    """Rows on both sides of every count at which another form takes over, with long and short sequences side by side."""
+    lens = [0, 1, 130, 1290, 128, 700, 15, 1291, 256]
+    _check_attention(_attention_case(T * G, len(lens), T, 3, G, D, 1291, fmt, new=True, tree=T % 2 == 0, lens=lens))
+    _check_attention(_attention_case(T + G, 2, T, 1, G, D, 390, fmt, new=False, lens=[390, 257]))
+
+
+@pytest.mark.parametrize("B,T,G,L,prefix", [(220, 3, 4, 90, 0), (220, 5, 5, 200, 0), (220, 6, 7, 300, 0), (230, 10, 6, 140, 0),
+                                            (60, 3, 4, 300, 300), (130, 5, 6, 129, 128), (90, 9, 5, 40, 1000),
+                                            (40, 16, 8, 260, 257)])
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_attention_many_segments(B, T, G, L, prefix, fmt):
+    """More segments than CTAs, most of them short, alone and behind a prefix that has blocks of rows of its own."""
+    lens = [(b * 37 + b * b) % (L + 1) for b in range(B)]
+    _check_attention(_attention_case(B + T, B, T, 2, G, 128, L, fmt, prefix=prefix, tree=True, lens=lens))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("B,H,L", [(1, 1, 1), (1, 2, 1152), (1, 2, 1281), (19, 8, 1152), (51, 3, 130), (152, 1, 1281)])
+def test_attention_few_segments_whole_and_cut(B, H, L, fmt):
+    """Segment counts and lengths on both sides of those that are not cut."""
+    for T, G in ((1, 7), (4, 10), (40, 4)):
+        _check_attention(_attention_case(B + L, B, T, H, G, 64, L, fmt, lens=[L - b % 2 for b in range(B)]))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128])
 def test_attention_lengths_at_tile_borders(fmt, D):
     lens = [0, 1, 2, 63, 64, 65, 127, 128, 129, 255, 256, 257, 384, 400]
     _check_attention(_attention_case(5, len(lens), 3, 2, 2, D, 400, fmt, lens=lens, tree=True))

@@ -86,7 +86,6 @@ constexpr int kSoloSegments = 152, kSoloTiles = 10;  // a CTA each for segments 
 constexpr int kMaxCtas = 160;         // of the grid; the workspace counts on it
 constexpr uint32_t kTmemCols = 512;
 constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr uint32_t kHintNs = 100000;
 constexpr int kMaxStages = 6;
 
 template <int D, bool E4> struct Cfg {
@@ -115,7 +114,8 @@ struct AttnParams {
     int solo;               // a CTA for each segment: nothing is cut
     int join_all;           // every row has parts elsewhere: nothing is written directly
     int seg_cost;           // what a segment counts beside its tiles, in tiles
-    int prefix_cost;        // the same of the line that the prefix segments are on (for the joining kernel)
+    int prefix_cost;        // the same of the prefix's
+    int prefix_two;         // 1: a prefix tile is two units
     int tma_q;              // a sequence's rows fit one slot: their queries come by TMA
     int nbp, ntp, UP;       // prefix: row blocks and tiles a head, units in all
     int nbs;                // row blocks of a sequence's rows
@@ -255,13 +255,13 @@ struct Walk {
         raw_next = raw_len(p, b + 1);
     }
 
-    // Tiles of [u, u1) in the segment of units us .. us + cost + nt - 1; moves u to its end.
-    __device__ void cut(Seg &s, int us, int cost)
+    // Tiles that begin in [u, u1) of the segment of units us .. us + cost + (nt << two) - 1; moves u to its end.
+    __device__ void cut(Seg &s, int us, int cost, int two)
     {
-        const int e = min(u1, us + cost + s.nt);
+        const int e = min(u1, us + cost + (s.nt << two));
         s.first = u0 >= us;
-        s.t0 = max(u - us - cost, 0);
-        s.n = max(e - us - cost, 0) - s.t0;
+        s.t0 = (max(u - us - cost, 0) + two) >> two;
+        s.n = ((max(e - us - cost, 0) + two) >> two) - s.t0;
         u = e;
     }
 
@@ -269,7 +269,7 @@ struct Walk {
     {
         while (u < u1) {
             if (u < p.UP) {
-                const int per = p.ntp + p.seg_cost;
+                const int per = (p.ntp << p.prefix_two) + p.prefix_cost;
                 s.id = u / per;
                 s.nt = p.ntp;
                 s.prefix = true;
@@ -281,7 +281,7 @@ struct Walk {
                 s.nrows = min(2 * kTile, p.B * p.T * p.G - s.row0);
                 s.keys = p.Lp;
                 s.hn = 0;
-                cut(s, s.id * per, p.seg_cost);
+                cut(s, s.id * per, p.prefix_cost, p.prefix_two);
             } else {
                 const Len len = clean_len(p, raw);
                 s.nt = tiles_of(p, len.n);
@@ -297,7 +297,7 @@ struct Walk {
                 s.keys = len.n;
                 s.hn = p.has_new;
                 s.id = (b * p.H + s.h) * p.nbs + s.rb;
-                cut(s, ub + rel * per, p.seg_cost);
+                cut(s, ub + rel * per, p.seg_cost, 0);
                 if (u == ub + p.H * p.nbs * per) {
                     ub = u;
                     ++b;
@@ -354,18 +354,32 @@ template <int D, bool E4> struct Fills {
     }
 };
 
+// A role's place in the ring of stages.
+template <int kStages> struct Ring {
+    uint32_t st = 0, phase = 0;  // stage; how often it has been used before, mod 2
+    __device__ __forceinline__ void step(uint32_t by)
+    {
+        st += by;
+        if (st >= (uint32_t)kStages) {
+            st -= kStages;
+            phase ^= 1u;
+        }
+    }
+};
+
 // ---- waits -------------------------------------------------------------------------
 
 // Waits for phase n (counted from 0) of the barrier; after a wait that gave up
 // every later one returns at once, so that each role still ends.  The timer is
-// read only after many tries: reading it costs more than a usual wait.
+// read only after many tries: reading it costs more than a usual wait.  No hint of a
+// time goes with the try: with one a waiting warp sleeps and wakes late (128 sequences of 4096 e4m3 keys 168 us, 180 with).
 template <class C> __device__ __forceinline__ void await(C &ctl, uint64_t *bar, uint32_t n)
 {
-    if (mbar_try_wait_hint(bar, n & 1u, kHintNs))
+    if (mbar_try_wait(bar, n & 1u))
         return;
     uint64_t t0 = 0;
     for (uint32_t it = 1;; ++it) {
-        if (mbar_try_wait_hint(bar, n & 1u, kHintNs))
+        if (mbar_try_wait(bar, n & 1u))
             return;
         if ((it & 15u) == 0) {
             if (*(volatile int *)&ctl.abort)
@@ -727,7 +741,8 @@ template <int kStages, int kQBufs, class Ct> __device__ __forceinline__ void fin
     }
 }
 
-// Where a segment's partial rows go: O [rows][D], then (R, l) of each; rows is the slot's.
+// Where a segment's partial rows go: O as [D / 4][rows][4], so that threads with a row each write side by side, then (R, l) of
+// each; rows is the slot's.
 template <int D> __device__ __forceinline__ float *part_of(const AttnParams &p, const Seg &seg, int &rows)
 {
     if (!seg.whole()) {
@@ -867,48 +882,52 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
         const uint64_t dKV8 = smem_desc(ring, 16, kAtom8, kSw8);
         const uint32_t tmu = __shfl_sync(0xffffffffu, tmem, 0);
         const bool issue = elect_one();
-        uint32_t base = 0;                  // ring fills before this segment
-        uint32_t nq = 0, npv[2] = {0, 0}, ntq = 0;
+        // One warp fetches these instructions for itself, so a job's are kept few: the ring is stepped through, not
+        // divided; what a segment is made of becomes one word of flags.
+        Ring<kStages> kr, vr;               // where the next scores and the next product find their tile
+        uint32_t nq = 0, npv = 0, ntq = 0;  // npv: phases of the slots' p_full, a bit each
         bool by_threads = false;
         uint32_t iseg = 0;
         while (next_seg(ctl, iseg, seg)) {
             if (seg.none())
                 continue;
-            const bool pair = seg.pair(), draft = seg.draft();
+            const bool pair = seg.pair(), draft = seg.draft(), tq = seg.tq;
             const int njobs = pair ? 2 * seg.n : seg.n;
-            const uint32_t qb = seg.tq ? ntq & 1u : 0u;
-            if (seg.tq && ntq == 0 && by_threads && issue) {
+            const uint32_t qb = tq ? ntq & 1u : 0u;
+            if (tq && ntq == 0 && by_threads && issue) {
                 tc_commit(&ctl.q_empty[0]);  // the earlier segments' products with Q
                 tc_commit(&ctl.q_empty[1]);
             }
             __syncwarp();
-            if (seg.tq && (!E4 || draft))
+            if (tq && (!E4 || draft))
                 await(ctl, &ctl.qt_full[qb], ntq >> 1);
             else
                 await(ctl, &ctl.q_full, nq++);
-            ntq += seg.tq;
-            by_threads |= !seg.tq;
+            ntq += tq;
+            by_threads |= !tq;
             bool q8 = E4 && !draft;
+            // the job whose values have to be cleared first: the new tokens', the last cached tile's (its end may be behind the length)
+            const int end = !seg.prefix && seg.valid(seg.t0 + seg.n - 1) < kTile ? (pair ? njobs - 2 : njobs - 1) : INT_MAX;
+            const int drafts = draft ? (pair ? 2 : 1) : 0;  // jobs of the new tokens
+            const uint64_t q0 = dQ + __shfl_sync(0xffffffffu, pair ? 0u : qb, 0) * (uint32_t)(C::kQTile / 16);
+            const uint32_t qstep = __shfl_sync(0xffffffffu, pair ? (uint32_t)(C::kQTile / 16) : 0u, 0);  // from slot 0's rows to slot 1's
             auto scores = [&](int q) {
-                const int i = pair ? q >> 1 : q, s = q & 1;
-                const bool dr = draft && i == 0;
+                const uint32_t s = __shfl_sync(0xffffffffu, (uint32_t)q & 1u, 0), st = __shfl_sync(0xffffffffu, kr.st, 0);
+                const bool dr = E4 && q < drafts, two = Fills<D, E4>::two(dr), last = !pair || s;  // last job of the tile
                 if (E4 && !dr && !q8) {
                     await(ctl, &ctl.q_full, nq++);
                     q8 = true;
                 }
-                const uint32_t f = base + Fills<D, E4>::at(seg, i);
-                const uint32_t st = __shfl_sync(0xffffffffu, f % kStages, 0);
-                await(ctl, &ctl.full[st], f / kStages);
+                await(ctl, &ctl.full[st], kr.phase);
                 tc_fence_after();
-                const uint32_t qs = __shfl_sync(0xffffffffu, pair ? (uint32_t)s : qb, 0);
-                const uint32_t d = tmu + 256 + 128 * __shfl_sync(0xffffffffu, s, 0);
-                const uint64_t q0 = dQ + qs * (uint32_t)(C::kQTile / 16);
+                const uint32_t d = tmu + 256 + 128 * s;
+                const uint64_t qd = q0 + s * qstep;
                 if (issue) {
                     if (!E4 || dr) {
                         const uint64_t k0 = dK + st * (uint32_t)(kSlotBytes / 16);
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk)
-                            tc_mma_bf16(d, q0 + (uint32_t)(kPanel / 16 * (kk / 4) + 2 * (kk & 3)),
+                            tc_mma_bf16(d, qd + (uint32_t)(kPanel / 16 * (kk / 4) + 2 * (kk & 3)),
                                         k0 + (uint32_t)(kPanel / 16 * (kk / 4) + 2 * (kk & 3)), idS, kk != 0);
                     } else {
                         const uint64_t k0 = dKV8 + st * (uint32_t)(kSlotBytes / 16);
@@ -916,26 +935,27 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
                         for (int part = 0; part < 2; ++part)  // the second term: the next panel (D = 128), or the other half of the same rows
 #pragma unroll
                             for (int kk = 0; kk < D / 32; ++kk)
-                                tc_mma_f8(d, q0 + (uint32_t)(part * (D == 128 ? kPanel / 16 : 4) + 2 * kk), k0 + 2u * kk, idS8,
+                                tc_mma_f8(d, qd + (uint32_t)(part * (D == 128 ? kPanel / 16 : 4) + 2 * kk), k0 + 2u * kk, idS8,
                                           part || kk);
                     }
                     tc_commit(&ctl.s_full[s]);
-                    if (seg.tq && q == njobs - 1)
+                    if (tq && q == njobs - 1)
                         tc_commit(&ctl.q_empty[qb]);
-                    if (Fills<D, E4>::two(dr) && (!pair || s == 1))
+                    if (two && last)
                         tc_commit(&ctl.empty[st]);  // no later job reads these keys
                 }
                 __syncwarp();
+                if (last)
+                    kr.step(two ? 2 : 1);
             };
             auto product = [&](int q) {
-                const int i = pair ? q >> 1 : q, s = q & 1;
-                const bool dr = draft && i == 0, two = Fills<D, E4>::two(dr);
-                const uint32_t f = base + Fills<D, E4>::at(seg, i) + (two ? 1 : 0);
-                const uint32_t st = __shfl_sync(0xffffffffu, f % kStages, 0);
-                await(ctl, &ctl.full[st], f / kStages);
-                if (dr || (!seg.prefix && seg.valid(seg.t0 + i) < kTile))
-                    await(ctl, &ctl.fix[st], f / kStages);
-                await(ctl, &ctl.p_full[s], npv[s]++);
+                const uint32_t s = __shfl_sync(0xffffffffu, (uint32_t)q & 1u, 0), st = __shfl_sync(0xffffffffu, vr.st, 0);
+                const bool dr = q < drafts, two = Fills<D, E4>::two(dr), last = !pair || s;
+                await(ctl, &ctl.full[st], vr.phase);
+                if (dr || q >= end)
+                    await(ctl, &ctl.fix[st], vr.phase);
+                await(ctl, &ctl.p_full[s], npv >> s);
+                npv ^= 1u << s;
                 if (dr && q == 0) {  // only now: the last segment's has been read
                     if (lane < 4)
                         ctl.poison[lane] = ctl.poison_slot[st][lane];
@@ -944,9 +964,9 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
                         mbar_arrive(&ctl.poison_full);
                 }
                 tc_fence_after();
-                const uint32_t su = __shfl_sync(0xffffffffu, s, 0);
-                const uint32_t v = st * (uint32_t)(kSlotBytes / 16) + __shfl_sync(0xffffffffu, two ? 0u : (uint32_t)(kVoff / 16), 0);
-                const uint32_t d = tmu + 128 * su, a = tmu + 256 + 128 * su;
+                const uint32_t v = st * (uint32_t)(kSlotBytes / 16) + (E4 ? __shfl_sync(0xffffffffu, two ? 0u : (uint32_t)(kVoff / 16), 0)
+                                                                          : Fills<D, E4>::two(false) ? 0u : (uint32_t)(kVoff / 16));
+                const uint32_t d = tmu + 128 * s, a = tmu + 256 + 128 * s;
                 const uint32_t acc = q >= 2;  // the slot's first job of the segment overwrites O
                 if (issue) {
                     if (!E4 || dr) {
@@ -964,11 +984,15 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
                                              acc | (kk != 0) | (part != 0));
                     }
                     tc_commit(&ctl.o_full[s]);
-                    if (!pair || s == 1)
+                    if (last)
                         tc_commit(&ctl.empty[st]);
                 }
                 __syncwarp();
+                if (last)
+                    vr.step(Fills<D, E4>::two(false) ? 2 : 1);
             };
+            if (Fills<D, E4>::two(draft))
+                vr.step(1);  // values behind keys: a stage further
             scores(0);
             if (njobs > 1)
                 scores(1);
@@ -977,7 +1001,7 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
                 if (q + 2 < njobs)
                     scores(q + 2);
             }
-            base += Fills<D, E4>::at(seg, seg.n - 1) + (Fills<D, E4>::two(draft && seg.n == 1) ? 2 : 1);
+            vr = kr;
         }
         if (issue)
             tc_commit(&ctl.done);
@@ -1313,12 +1337,12 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
                 const bool valid_row = r < rows;
                 const bool direct = !p.join_all && seg.whole();
                 const int cs = pair ? 0 : s * (D / 2), ce = pair ? D : cs + D / 2;
-                float *part = nullptr;
+                float4 *part = nullptr;
+                int nr = 0;
                 if (!direct) {
                     const int rr = r + (pair ? kTile * s : 0);
-                    int nr;
                     float *slot = part_of<D>(p, seg, nr);
-                    part = slot + (size_t)rr * D;
+                    part = reinterpret_cast<float4 *>(slot) + rr;
                     if (valid_row && (pair || s == 0))
                         *reinterpret_cast<float2 *>(slot + (size_t)nr * D + rr * 2) = make_float2(R, l);
                 }
@@ -1356,10 +1380,10 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
                                 dst[k] = make_uint4(pack_bf16(o[8 * k], o[8 * k + 1]), pack_bf16(o[8 * k + 2], o[8 * k + 3]),
                                                     pack_bf16(o[8 * k + 4], o[8 * k + 5]), pack_bf16(o[8 * k + 6], o[8 * k + 7]));
                         } else {
-                            float4 *dst = reinterpret_cast<float4 *>(part + c0);
+                            float4 *dst = part + (c0 / 4) * nr;
 #pragma unroll
                             for (int k = 0; k < 8; ++k)
-                                dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                                dst[k * nr] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
                         }
                     }
                 }
@@ -1431,48 +1455,29 @@ struct Parts {
     int rows, wrows;              // rows of a slot
     int c0, n, tail;              // tail: the first part is the last of its CTA's stretch, not the first
 
-    // The segment's units are us .., its nt tiles those from t0 on, in a line of U units cut for C CTAs.  Of the CTAs
+    // The segment's units are us .., its tiles begin at units from .. to, in a line of U units cut for C CTAs.  Of the CTAs
     // only the first can have begun with another segment.
-    __device__ __forceinline__ void find(int us, int t0, int nt, int U, int C)
+    __device__ __forceinline__ void find(int us, int from, int to, int U, int C)
     {
-        c0 = owner(t0, U, C);
-        n = owner(t0 + nt - 1, U, C) - c0 + 1;
+        c0 = owner(from, U, C);
+        n = owner(to, U, C) - c0 + 1;
         tail = stretch(c0, U, C) < us;
     }
 
-    template <int D> __device__ __forceinline__ const float *at(int i, int rr, float2 &ml) const
+    // Row rr of part i.
+    template <int D> __device__ __forceinline__ const float4 *at(int i, int rr, float2 &ml, int &nr) const
     {
         const bool one = n == 1;
-        const int nr = one ? wrows : rows;
+        nr = one ? wrows : rows;
         const float *slot = one ? whole : pieces + (size_t)(2 * (c0 + i) + (i == 0 ? tail : 0)) * nr * (D + 4);
         ml = __ldg(reinterpret_cast<const float2 *>(slot + (size_t)nr * D + rr * 2));
-        return slot + (size_t)rr * D;
+        return reinterpret_cast<const float4 *>(slot) + rr;
     }
 };
 
-template <int D> struct Joined {
-    static constexpr int E = D / 32;  // columns of a lane
-    float top, l, acc[E];
-
-    __device__ __forceinline__ void start()
-    {
-        top = -INFINITY;
-        l = 0.0f;
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            acc[e] = 0.0f;
-    }
-
-    __device__ __forceinline__ static void load(const float *o, int lane, float *v)
-    {
-        if constexpr (E == 4) {
-            const float4 x = __ldg(reinterpret_cast<const float4 *>(o) + lane);
-            v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-        } else {
-            const float2 x = __ldg(reinterpret_cast<const float2 *>(o) + lane);
-            v[0] = x.x, v[1] = x.y;
-        }
-    }
+// E of a row's columns in a thread.
+template <int E> struct Joined {
+    float top = -INFINITY, l = 0.0f, acc[E] = {};
 
     // Takes part (R, l) = ml with values v in.
     __device__ __forceinline__ void add(float2 ml, const float *v)
@@ -1485,26 +1490,24 @@ template <int D> struct Joined {
             acc[e] = acc[e] * fo + (fn == 0.0f ? 0.0f : fn * v[e]);
         top = mn;
     }
-
-    __device__ __forceinline__ void write(const AttnParams &p, long long row, int lane) const
+    __device__ __forceinline__ float inverse() const
     {
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        __nv_bfloat16 *dst = p.out + row * D + lane * E;
-        if constexpr (E == 4)
-            *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
-        else
-            *reinterpret_cast<unsigned *>(dst) = pack_bf16(acc[0] * inv, acc[1] * inv);
-        if (p.lse && lane == 0)
-            p.lse[row] = l == 0.0f ? -INFINITY : (top + log2f(l)) * 0.69314718055994531f;
+        return l == 0.0f ? 0.0f : 1.0f / l;
+    }
+    __device__ __forceinline__ float lse() const
+    {
+        return l == 0.0f ? -INFINITY : (top + log2f(l)) * 0.69314718055994531f;
     }
 };
 
-// With a prefix every row has parts to join.  Grid: x = (sequence, head), y = 32 of its rows, 4 to a warp.  The
-// 64-bit divisions behind a segment's CTAs are done once for the 4, those of the segments in lanes side by side;
-// the 4 rows' loads are in flight together.
+// With a prefix every row has parts to join.  Grid: x = (sequence, head), y = 32 of its rows, 4 to a warp: 8 lanes
+// a row, so that a load takes whole sectors of the parts' 16-byte pieces.  The 64-bit divisions behind a segment's CTAs are
+// done once for the 4 rows, those of the segments in lanes side by side.  128 sequences' 112 rows of 4 heads, 2 to 3 parts
+// each (29 MB a part): 24 us, 32 with lanes side
+// by side along a row of [rows][D] parts, whose writers then were 10 us slower.
 template <int D> __global__ void __launch_bounds__(256, 3) sv_attention_join_kernel(AttnParams p, int grid, PrefixLine px)
 {
-    constexpr int kR = 4;
+    constexpr int kR = 4, kV = D / 32;
     grid_dependency_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int b = blockIdx.x / p.H, h = blockIdx.x - b * p.H, nrows = p.T * p.G;
@@ -1521,13 +1524,12 @@ template <int D> __global__ void __launch_bounds__(256, 3) sv_attention_join_ker
     Parts q;
     {
         const int cost = k ? p.prefix_cost : p.seg_cost;
-        const int us = k ? id_p * (p.ntp + cost) : ub + (h * p.nbs + rb) * (nt + cost);
-        q.find(us, us + cost, k ? p.ntp : nt, k && px.U ? px.U : U, k && px.U ? px.C : C);
+        const int us = k ? id_p * ((p.ntp << p.prefix_two) + cost) : ub + (h * p.nbs + rb) * (nt + cost);
+        q.find(us, us + cost, us + cost + (k ? (p.ntp - 1) << p.prefix_two : nt - 1), k && px.U ? px.U : U, k && px.U ? px.C : C);
     }
-    Joined<D> j[kR];
-#pragma unroll
-    for (int r = 0; r < kR; ++r)
-        j[r].start();
+    const int row = local + min(lane & 3, last), x = lane >> 2;  // this lane's row; its pieces are x, x + 8, ..
+    const int Rp = b * nrows + row;
+    Joined<4 * kV> j;
     // the sources in turn; rows that are not of this one take its part as one without keys
 #pragma unroll 1
     for (int src = 0; src < 3; ++src) {
@@ -1542,28 +1544,34 @@ template <int D> __global__ void __launch_bounds__(256, 3) sv_attention_join_ker
         t.wrows = src ? p.rp : p.rs;
         t.pieces = src && px.U ? px.pieces : p.pieces;
         t.rows = p.rm;
-#pragma unroll 1
+        const int rr = (src ? Rp : row) % (2 * kTile);
+        const bool mine = !src || Rp / (2 * kTile) - block0 == src - 1;
+#pragma unroll 2
         for (int i = 0; i < t.n; ++i) {
-            float2 ml[kR];
-            float v[kR][Joined<D>::E];
+            float2 ml;
+            int nr;
+            float v[4 * kV];
+            const float4 *at = t.at<D>(i, rr, ml, nr);
+            at += x * nr;
 #pragma unroll
-            for (int r = 0; r < kR; ++r) {
-                const int row = min(r, last);
-                j[r].load(t.at<D>(i, (src ? R0 + row : local + row) % (2 * kTile), ml[r]), lane, v[r]);
-                if (src && (R0 + row) / (2 * kTile) - block0 != src - 1)
-                    ml[r] = make_float2(-INFINITY, 0.0f);
+            for (int c = 0; c < kV; ++c) {
+                const float4 y = __ldg(at + 8 * c * nr);
+                v[4 * c] = y.x, v[4 * c + 1] = y.y, v[4 * c + 2] = y.z, v[4 * c + 3] = y.w;
             }
-#pragma unroll
-            for (int r = 0; r < kR; ++r)
-                j[r].add(ml[r], v[r]);
+            j.add(mine ? ml : make_float2(-INFINITY, 0.0f), v);
         }
     }
+    if ((lane & 3) > last)
+        return;
+    const float inv = j.inverse();
+    const int tok = row / p.G;
+    const long long orow = ((long long)b * p.T + tok) * p.Hq + h * p.G + (row - tok * p.G);
 #pragma unroll
-    for (int r = 0; r < kR; ++r)
-        if (r <= last) {
-            const int tok = (local + r) / p.G;
-            j[r].write(p, ((long long)b * p.T + tok) * p.Hq + h * p.G + (local + r - tok * p.G), lane);
-        }
+    for (int c = 0; c < kV; ++c)
+        *reinterpret_cast<uint2 *>(p.out + orow * D + (x + 8 * c) * 4) =
+            make_uint2(pack_bf16(j.acc[4 * c] * inv, j.acc[4 * c + 1] * inv), pack_bf16(j.acc[4 * c + 2] * inv, j.acc[4 * c + 3] * inv));
+    if (p.lse && x == 0)
+        p.lse[orow] = j.lse();
 }
 
 // Without a prefix only the segments that a stretch's end cuts have parts.  Grid: x = those ends, y = rows; W
@@ -1580,7 +1588,7 @@ template <int D, int W> __global__ void __launch_bounds__(256) sv_attention_join
     if (cut.x < 0 || rr >= cut.y)
         return;
     Parts sp;
-    sp.find(cut.z - p.seg_cost, cut.z, cut.w, U, min(grid, U));
+    sp.find(cut.z - p.seg_cost, cut.z, cut.z + cut.w - 1, U, min(grid, U));
     // one end of those that cut this segment does the work: the first
     if (sp.c0 != (int)blockIdx.x - 1)
         return;
@@ -1588,13 +1596,21 @@ template <int D, int W> __global__ void __launch_bounds__(256) sv_attention_join
     sp.wrows = 0;
     sp.pieces = p.pieces;
     sp.rows = p.rm;
-    Joined<D> j;
-    j.start();
-    float2 ml;
+    Joined<E> j;  // columns E * lane ..
 #pragma unroll 2
     for (int i = W == 1 ? 0 : warp; i < sp.n; i += W) {
+        float2 ml;
+        int nr;
         float v[E];
-        j.load(sp.at<D>(i, rr, ml), lane, v);
+        const float4 *piece = sp.at<D>(i, rr, ml, nr);
+        const float *at = reinterpret_cast<const float *>(piece + lane * E / 4 * nr) + lane * E % 4;
+        if constexpr (E == 4) {
+            const float4 y = __ldg(reinterpret_cast<const float4 *>(at));
+            v[0] = y.x, v[1] = y.y, v[2] = y.z, v[3] = y.w;
+        } else {
+            const float2 y = __ldg(reinterpret_cast<const float2 *>(at));
+            v[0] = y.x, v[1] = y.y;
+        }
         j.add(ml, v);
     }
     if constexpr (W > 1) {
@@ -1629,7 +1645,15 @@ template <int D, int W> __global__ void __launch_bounds__(256) sv_attention_join
             j.acc[e] = acc[e];
     }
     const int R = cut.x + rr, tok = R / p.G;
-    j.write(p, (long long)tok * p.Hq + h * p.G + (R - tok * p.G), lane);
+    const long long orow = (long long)tok * p.Hq + h * p.G + (R - tok * p.G);
+    const float inv = j.inverse();
+    __nv_bfloat16 *dst = p.out + orow * D + lane * E;
+    if constexpr (E == 4)
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(j.acc[0] * inv, j.acc[1] * inv), pack_bf16(j.acc[2] * inv, j.acc[3] * inv));
+    else
+        *reinterpret_cast<unsigned *>(dst) = pack_bf16(j.acc[0] * inv, j.acc[1] * inv);
+    if (p.lse && lane == 0)
+        p.lse[orow] = j.lse();
 }
 
 // ---- host side -------------------------------------------------------------------------
@@ -1670,10 +1694,16 @@ bool make_map(CUtensorMap *m, const void *base, bool codes, int64_t B, int64_t n
     const cuuint64_t strides[3] = {(cuuint64_t)D * es, (cuuint64_t)sn * es, (cuuint64_t)sb * es};
     const cuuint32_t box[4] = {(cuuint32_t)(codes ? D : 64), (cuuint32_t)box_heads, (cuuint32_t)box_n, 1};
     const cuuint32_t estr[4] = {1, 1, 1, 1};
+    // what a miss brings into the L2: a head's row, not its neighbour's too, which has left the cache when its turn comes (rows of
+    // 128 bytes: 128 sequences of 4096 e4m3 keys 212 us with 256, 180 with this)
+    const int64_t row = D * (codes ? 1 : 2);
+    const CUtensorMapL2promotion promote = row >= 256   ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                                           : row >= 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                                        : CU_TENSOR_MAP_L2_PROMOTION_L2_64B;
     return enc(m, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base),
                dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                codes && D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+               promote, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 sv_status check(const sv_attention_args *a)
@@ -1693,7 +1723,7 @@ sv_status check(const sv_attention_args *a)
 
 // Sizes of a call, false when they pass the 32-bit counts of the kernels.
 struct Plan {
-    int G, nbp, ntp, nbs, rp, rs, rm, seg_cost, prefix_cost;
+    int G, nbp, ntp, nbs, rp, rs, rm, seg_cost, prefix_cost, prefix_two;
     bool solo;         // few short segments: a CTA each, in one launch
     bool split;        // an e4m3 prefix for many rows: in bf16, on a line and in a launch of its own
     int64_t UP, most;  // prefix units, units at full lengths
@@ -1712,11 +1742,16 @@ bool plan(const sv_attention_args &a, Plan &w)
     w.nbs = (int)((seq_rows + 2 * kTile - 1) / (2 * kTile));
     // A segment's start and end (queries, epilogue) against a tile, so that short segments and long ones fill the
     // stretches alike.  Measured: 256 chains of 8 over up to 2048 keys 124, 116, 114 us with 1, 2, 3; of 6 over 4096 e4m3
-    // keys 282, 261, 253, 248 us with 1, 3, 4, 6; with a prefix (long segments, all alike) 1 is best, 108 against 111 us.
+    // keys 243, 232, 227, 227 us with 3, 4, 5, 6.
     w.split = a.format == SV_KV_E4M3 && a.prefix_len > 0 && w.nbp >= 2;
-    w.seg_cost = a.prefix_len > 0 && !w.split ? 1 : a.format == SV_KV_E4M3 && seq_rows <= kNarrowMost ? 6 : 3;
-    w.prefix_cost = 1;
-    w.UP = a.prefix_len > 0 ? a.heads_kv * w.nbp * (w.ntp + w.prefix_cost) : 0;  // below 2^31 * 2^24
+    w.seg_cost = a.format == SV_KV_E4M3 && !(a.prefix_len > 0 && !w.split) && seq_rows <= kNarrowMost ? 6 : 3;
+    // A prefix tile is 256 rows' work, twice that of a sequence's tile of up to 128 rows beside it.  64 sequences' 56 rows
+    // over a prefix of 8192 keys: with one unit for either and costs of 1 the CTAs' times lie between 0.7 and 1.2 of the
+    // mean and the call takes 101.9 us; with two units and costs of 3 and 6, 95.6.  On a line of its own (128 sequences' 112
+    // rows over 2048 keys) a segment costs 8 tiles' time: 180.5 us with 1, 178.4 with 3, 172.2 with 8.
+    w.prefix_cost = w.split ? 8 : 6;
+    w.prefix_two = !w.split && rows > kTile && seq_rows <= kTile && 2 * a.heads_kv * w.nbp * w.ntp >= 2 * kMaxCtas;
+    w.UP = a.prefix_len > 0 ? a.heads_kv * w.nbp * (((int64_t)w.ntp << w.prefix_two) + w.prefix_cost) : 0;  // below 2^31 * 2^25
     if (a.prefix_len > big / (a.heads_kv * a.head_dim))
         return false;
     const int64_t tiles = (a.max_len + kTile - 1) / kTile + 1 + w.seg_cost;
@@ -1762,7 +1797,8 @@ template <int D> cudaError_t set_attr()
     const void *kernels[5] = {(const void *)sv_attention_kernel<D, false>, (const void *)sv_attention_kernel<D, true>,
                               (const void *)sv_attention_narrow_kernel<D, 8>, (const void *)sv_attention_narrow_kernel<D, 16>,
                               (const void *)sv_attention_narrow_kernel<D, 24>};
-    const size_t bytes[5] = {smem_bytes<D, false>(), smem_bytes<D, true>(), narrow_smem<D>(), narrow_smem<D>(), narrow_smem<D>()};
+    const size_t bytes[5] = {smem_bytes<D, false>(), smem_bytes<D, true>(), narrow_smem<D, 8>(),
+                             narrow_smem<D, 16>(), narrow_smem<D, 24>()};
     for (int i = 0; i < 5; ++i) {
         const cudaError_t e = cudaFuncSetAttribute(kernels[i], cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes[i]);
         if (e != cudaSuccess)
@@ -1807,16 +1843,20 @@ cudaLaunchConfig_t config(unsigned x, unsigned y, int threads, size_t smem, cuda
     return cfg;
 }
 
+template <int D, int RW> cudaError_t launch_narrow(const Maps &maps, const AttnParams &p, int C, cudaStream_t st)
+{
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = config((unsigned)C, 1, kNarrowThreads, narrow_smem<D, RW>(), st, attr);
+    return cudaLaunchKernelEx(&cfg, sv_attention_narrow_kernel<D, RW>, maps, p);
+}
+
 template <int D, bool E4> cudaError_t launch_rows(const Maps &maps, const AttnParams &p, int C, cudaStream_t st)
 {
     cudaLaunchAttribute attr[1];
     const int rows = p.T * p.G;
     // 8-bit caches and few rows: the products turned around (attention_narrow.cuh)
     if (E4 && p.UP == 0 && rows <= kNarrowMost) {
-        const cudaLaunchConfig_t cfg = config((unsigned)C, 1, kNarrowThreads, narrow_smem<D>(), st, attr);
-        return rows <= 16   ? cudaLaunchKernelEx(&cfg, sv_attention_narrow_kernel<D, 8>, maps, p)
-               : rows <= 32 ? cudaLaunchKernelEx(&cfg, sv_attention_narrow_kernel<D, 16>, maps, p)
-                            : cudaLaunchKernelEx(&cfg, sv_attention_narrow_kernel<D, 24>, maps, p);
+        return rows <= 16 ? launch_narrow<D, 8>(maps, p, C, st) : rows <= 32 ? launch_narrow<D, 16>(maps, p, C, st) : launch_narrow<D, 24>(maps, p, C, st);
     }
     const cudaLaunchConfig_t cfg = config((unsigned)C, 1, kThreads, smem_bytes<D, E4>(), st, attr);
     return cudaLaunchKernelEx(&cfg, sv_attention_kernel<D, E4>, maps, p);
@@ -1906,6 +1946,7 @@ extern "C" sv_status spec_verify_attention(const sv_attention_args *args, void *
     p.join_all = a.prefix_len > 0;
     p.seg_cost = w.seg_cost;
     p.prefix_cost = w.prefix_cost;
+    p.prefix_two = w.prefix_two;
     p.tma_q = a.T * w.G <= kTile;
     if (p.tma_q) {  // box: one token range's rows of one head, 64 wide
         const int64_t st_ = a.T > 1 ? a.q_stride_t : qrow, sb_ = a.B > 1 ? a.q_stride_b : a.T * st_;
@@ -1971,7 +2012,6 @@ extern "C" sv_status spec_verify_attention(const sv_attention_args *args, void *
                                chunks, D / 16);
         AttnParams pp = p;
         pp.nb = 0;
-        pp.seg_cost = w.prefix_cost;
         pp.rm = w.rp;
         pp.pieces = reinterpret_cast<float *>(ws + w.off_pp);
         px = {(int)w.UP, ctas(w.UP), pp.pieces};

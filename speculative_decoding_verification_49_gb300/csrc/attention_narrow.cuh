@@ -35,8 +35,7 @@
 
 namespace {
 
-constexpr int kNarrowRows = 64, kNarrowStages = 4;
-constexpr int kNarrowPanel = kNarrowRows * 128;  // 64 rows of 128 bytes of Q
+constexpr int kNarrowStages = 5;                 // at most; as many as fit
 constexpr int kNarrowMost = 48;                  // rows that the kernel takes
 constexpr int kNarrowSoftmax = 512, kNarrowThreads = 640;
 constexpr int kNarrowAux = kNarrowSoftmax / 32;  // the first of the other warps
@@ -48,11 +47,16 @@ static_assert(kNarrowSoftmax * kNarrowRegsSoftmax + (kNarrowThreads - kNarrowSof
 // is 2^margin above the best of four keys.  e5m2's smallest step, 2^-16, is then at most 2^-20 of the row's largest weight.
 constexpr float kNarrowBase = 8.0f, kNarrowSlack = 7.0f, kNarrowMargin = 4.0f;
 
-template <int D> struct NarrowCfg {
-    static constexpr int kQ = kNarrowRows * D * 2;      // Q in bf16
-    static constexpr int kQC = kNarrowRows * D * 2;     // its codes: the first terms' rows, then the second's
-    static constexpr int kTerm = kTile * kNarrowRows;   // one term of a slot's weights
-    static constexpr int kP = 3 * kTerm;
+template <int D, int RW> struct NarrowCfg {
+    static constexpr int kN = 2 * RW;               // rows, padded: columns of S^T, of each part of O^T
+    static constexpr int kPanel = kN * 128;         // 128 bytes of all rows of Q
+    static constexpr int kQ = kN * D * 2;           // Q in bf16
+    static constexpr int kQC = kN * D * 2;          // its codes: the first terms' rows, then the second's
+    static constexpr int kAtom = kTile * 64;        // 64 columns of a slot's weights
+    static constexpr int kP = (RW == 24 ? 3 : 2) * kAtom;  // three terms in 8 bits, or (new tokens) 128 keys of 128 bytes
+    static constexpr int kFixed = kQ + kQC + 2 * kP;
+    static constexpr int kFit = (232448 - 6144 - kFixed) / kSlotBytes, kStages = kFit < kNarrowStages ? kFit : kNarrowStages;
+    static_assert(3 * kN * kTile <= kP && kStages >= 4, "what the products count on");
 };
 
 struct NarrowCtl {
@@ -71,19 +75,20 @@ struct NarrowCtl {
     int start_b, start_ub;
     SegRing segs;
     // per slot and row
-    alignas(16) float nmu[2][kNarrowRows];   // base - mu
-    alignas(16) float fac[2][kNarrowRows];   // the last move of the reference; at the end the slots' factors
+    alignas(16) float nmu[2][kNarrowMost];   // base - mu
+    alignas(16) float fac[2][kNarrowMost];   // the last move of the reference; at the end the slots' factors
     alignas(16) float part[4][4][32];        // per warpgroup and warp: sampled scores, maxima, sums of its rows
-    float mu[2][kNarrowRows], l[2][kNarrowRows];
+    float mu[2][kNarrowMost], l[2][kNarrowMost];
     uint16_t scale[kNarrowStages][kTile];    // of a stage's keys: K's scale byte, V's in the upper half
 };
 
-template <int D> constexpr size_t narrow_smem()
+static_assert(sizeof(NarrowCtl) <= 6144, "NarrowCfg::kStages counts on it");
+
+template <int D, int RW> constexpr size_t narrow_smem()
 {
-    using N = NarrowCfg<D>;
-    return (size_t)N::kQ + N::kQC + 2 * (size_t)N::kP + (size_t)kNarrowStages * kSlotBytes + sizeof(NarrowCtl);
+    using N = NarrowCfg<D, RW>;
+    return (size_t)N::kFixed + (size_t)N::kStages * kSlotBytes + sizeof(NarrowCtl);
 }
-static_assert(narrow_smem<128>() <= 232448, "227 KiB of shared memory per CTA");
 
 // Order-preserving map of floats to ints (a positive NaN is above everything).
 __device__ __forceinline__ int ordered(float x)
@@ -135,13 +140,13 @@ __device__ __forceinline__ float transpose_sum8(float *v, int lane)
 template <int D, int RW>
 __global__ void __launch_bounds__(kNarrowThreads, 1) sv_attention_narrow_kernel(const __grid_constant__ Maps maps, AttnParams p)
 {
-    using N = NarrowCfg<D>;
-    constexpr int kStages = kNarrowStages;
+    using N = NarrowCfg<D, RW>;
+    constexpr int kStages = N::kStages, kN = N::kN;
     extern __shared__ __align__(1024) unsigned char smem[];
     unsigned char *qc = smem + N::kQ, *pw = qc + N::kQC, *ring = pw + 2 * N::kP;
     NarrowCtl &ctl = *reinterpret_cast<NarrowCtl *>(ring + kStages * kSlotBytes);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int rows = p.T * p.G;  // of every segment, at most 64
+    const int rows = p.T * p.G;  // of every segment, at most kN
     const int ngroup = (rows + RW - 1) / RW;
 
     if (smem_u32(smem) & 1023u) {
@@ -199,15 +204,15 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) sv_attention_narrow_kernel(
             if (lane == 0) {
                 Walk walk;
                 walk.start(p, u0, u1, ctl.start_b, ctl.start_ub);
-                produce<D, true, kStages, 1, N::kQ, kNarrowPanel>(p, maps, ctl, walk, smem, ring);
+                produce<D, true, kStages, 1, N::kQ, N::kPanel>(p, maps, ctl, walk, smem, ring);
             }
             __syncwarp();
         } else if (warp == kNarrowAux + 1) {
             // ---- MMA issuer ----
             constexpr uint32_t kTr = (1u << 15) | (1u << 16);  // both operands MN-major
-            constexpr uint32_t idS = idesc_bf16_f32(kTile, kNarrowRows), idO = idS | kTr;
-            constexpr uint32_t idS8 = idesc_f8_f32(0, 0, kTile, kNarrowRows, 0);
-            constexpr uint32_t idO8 = idesc_f8_f32(0, 1, kTile, 3 * kNarrowRows, 0) | kTr;
+            constexpr uint32_t idS = idesc_bf16_f32(kTile, kN), idO = idS | kTr;
+            constexpr uint32_t idS8 = idesc_f8_f32(0, 0, kTile, kN, 0);
+            constexpr uint32_t idO8 = idesc_f8_f32(0, 1, kTile, 3 * kN, 0) | kTr;
             constexpr int kSw8 = D;
             constexpr uint32_t kAtom8 = 8 * D;
             const uint64_t dQ = smem_desc_k128(smem), dQ8 = smem_desc(qc, 16, kAtom8, kSw8);
@@ -215,64 +220,60 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) sv_attention_narrow_kernel(
             // V^T: M = 128 channels; with D = 64 the second 64 repeat the first (stride 0) and are not read
             const uint64_t dV = smem_desc(ring, D == 128 ? kPanel : 0, 1024, 128);
             const uint64_t dV8 = smem_desc(ring, D == 128 ? 16 : 0, kAtom8, kSw8);
-            const uint64_t dP = smem_desc(pw, 16, 1024, 128), dP8 = smem_desc(pw, N::kTerm, 512, 64);
+            const uint64_t dP = smem_desc(pw, 16, 1024, 128), dP8 = smem_desc(pw, N::kAtom, 512, 64);
             const uint32_t tmu = __shfl_sync(0xffffffffu, tmem, 0);
             const bool issue = elect_one();
-            uint32_t base = 0, nq = 0, np0 = 0, np1 = 0, nseg = 0, iseg = 0;
+            Ring<kStages> kr, vr;  // as in attention.cu
+            uint32_t nq = 0, npv = 0, nseg = 0, iseg = 0;
             while (next_seg(ctl, iseg, seg)) {
                 if (seg.none())
                     continue;
                 const bool draft = seg.draft();
-                const int njobs = seg.n;
+                const int njobs = seg.n, end = seg.valid(seg.t0 + seg.n - 1) < kTile ? njobs - 1 : INT_MAX;
                 if (draft)
                     await(ctl, &ctl.qt_full[0], nseg);
                 ++nseg;
-                bool q8 = false;
                 auto scores = [&](int q) {
-                    const uint32_t s = (uint32_t)q & 1u;
-                    const bool dr = draft && q == 0, first8 = !dr && !q8;
-                    if (first8) {
+                    const uint32_t s = __shfl_sync(0xffffffffu, (uint32_t)q & 1u, 0), st = __shfl_sync(0xffffffffu, kr.st, 0);
+                    const bool dr = draft && q == 0, two = Fills<D, true>::two(dr), first8 = q == (draft ? 1 : 0);
+                    if (first8)
                         await(ctl, &ctl.q_full, nq++);
-                        q8 = true;
-                    }
-                    const uint32_t f = base + Fills<D, true>::at(seg, q);
-                    const uint32_t st = __shfl_sync(0xffffffffu, f % kStages, 0);
-                    await(ctl, &ctl.full[st], f / kStages);
+                    await(ctl, &ctl.full[st], kr.phase);
                     tc_fence_after();
-                    const uint32_t d = tmu + 384 + 64 * __shfl_sync(0xffffffffu, s, 0);
+                    const uint32_t d = tmu + 384 + 64 * s;
                     if (issue) {
                         if (dr) {
                             const uint64_t k0 = dK + st * (uint32_t)(kSlotBytes / 16);
 #pragma unroll
                             for (int kk = 0; kk < D / 16; ++kk)
                                 tc_mma_bf16(d, k0 + (uint32_t)(kPanel / 16 * (kk / 4) + 2 * (kk & 3)),
-                                            dQ + (uint32_t)(kNarrowPanel / 16 * (kk / 4) + 2 * (kk & 3)), idS, kk != 0);
+                                            dQ + (uint32_t)(N::kPanel / 16 * (kk / 4) + 2 * (kk & 3)), idS, kk != 0);
                         } else {
                             const uint64_t k0 = dK8 + st * (uint32_t)(kSlotBytes / 16);
 #pragma unroll
                             for (int part = 0; part < 2; ++part)
 #pragma unroll
                                 for (int kk = 0; kk < D / 32; ++kk)
-                                    tc_mma_f8(d, k0 + 2u * kk, dQ8 + (uint32_t)(part * kNarrowRows * D / 16 + 2 * kk), idS8,
+                                    tc_mma_f8(d, k0 + 2u * kk, dQ8 + (uint32_t)(part * kN * D / 16 + 2 * kk), idS8,
                                               part || kk);
                         }
                         tc_commit(&ctl.s_full[s]);
                         if (first8 || (dr && njobs == 1))
                             tc_commit(&ctl.q_empty[0]);  // the codes are made and the new tokens' product is ahead of this
-                        if (Fills<D, true>::two(dr))
+                        if (two)
                             tc_commit(&ctl.empty[st]);
                     }
                     __syncwarp();
+                    kr.step(two ? 2 : 1);
                 };
                 auto product = [&](int q) {
-                    const uint32_t s = (uint32_t)q & 1u;
+                    const uint32_t s = __shfl_sync(0xffffffffu, (uint32_t)q & 1u, 0), st = __shfl_sync(0xffffffffu, vr.st, 0);
                     const bool dr = draft && q == 0, two = Fills<D, true>::two(dr);
-                    const uint32_t f = base + Fills<D, true>::at(seg, q) + (two ? 1 : 0);
-                    const uint32_t st = __shfl_sync(0xffffffffu, f % kStages, 0);
-                    await(ctl, &ctl.full[st], f / kStages);
-                    if (dr || seg.valid(seg.t0 + q) < kTile)
-                        await(ctl, &ctl.fix[st], f / kStages);
-                    await(ctl, &ctl.p_full[s], s ? np1++ : np0++);
+                    await(ctl, &ctl.full[st], vr.phase);
+                    if (dr || q >= end)
+                        await(ctl, &ctl.fix[st], vr.phase);
+                    await(ctl, &ctl.p_full[s], npv >> s);
+                    npv ^= 1u << s;
                     if (dr) {  // only now: the last segment's has been read
                         if (lane < 4)
                             ctl.poison[lane] = ctl.poison_slot[st][lane];
@@ -281,9 +282,8 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) sv_attention_narrow_kernel(
                             mbar_arrive(&ctl.poison_full);
                     }
                     tc_fence_after();
-                    const uint32_t su = __shfl_sync(0xffffffffu, s, 0);
                     const uint32_t v = st * (uint32_t)(kSlotBytes / 16) + __shfl_sync(0xffffffffu, two ? 0u : (uint32_t)(kVoff / 16), 0);
-                    const uint32_t d = tmu + 192 * su, pb = su * (uint32_t)(N::kP / 16);
+                    const uint32_t d = tmu + 192 * s, pb = s * (uint32_t)(N::kP / 16);
                     const uint32_t acc = q >= 2;  // a slot's first product of the segment overwrites O^T
                     if (issue) {
                         if (dr) {
@@ -299,7 +299,10 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) sv_attention_narrow_kernel(
                         tc_commit(&ctl.empty[st]);
                     }
                     __syncwarp();
+                    vr.step(1);
                 };
+                if (Fills<D, true>::two(draft))
+                    vr.step(1);  // values behind keys: a stage further
                 scores(0);
                 if (njobs > 1)
                     scores(1);
@@ -308,7 +311,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) sv_attention_narrow_kernel(
                     if (q + 2 < njobs)
                         scores(q + 2);
                 }
-                base += Fills<D, true>::at(seg, seg.n - 1) + (Fills<D, true>::two(draft && seg.n == 1) ? 2 : 1);
+                vr = kr;
             }
             if (issue)
                 tc_commit(&ctl.done);
@@ -377,16 +380,17 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) sv_attention_narrow_kernel(
         uint32_t nj = 0, npois = 0, nseg = 0, nconv = 0;
         uint32_t base = 0;  // ring fills before this segment
         uint32_t iseg = 0;
-        if (tid == 0)
-            hand_out_seg(ctl, 0);
-        bar_sync(1, kNarrowSoftmax);
-        while (get_seg(ctl.segs.cur[iseg & 1], seg)) {
-            ++iseg;
-            const bool draft = seg.draft(), none = seg.none();
-            const int njobs = none ? 0 : seg.n;
-            bool poison = false;
-            float cq = p.c;
-            if (!none) {
+        // Takes segment i and makes its codes of Q (all threads, before the epilogue of the last segment, so that the first scores
+        // are there when that is done).  Returns whether there is one; cq: factor of its scores.
+        auto take = [&](uint32_t i, float &cq) {
+            if (tid == 0)
+                hand_out_seg(ctl, i);
+            bar_sync(1, kNarrowSoftmax);  // and the last segment's codes have been read: all its scores have
+            if (!get_seg(ctl.segs.cur[i & 1], seg))
+                return false;
+            const bool draft = seg.draft();
+            cq = p.c;
+            if (!seg.none()) {
                 await(ctl, &ctl.qt_full[0], nseg++);
                 __syncwarp();
                 if (lane == 0)
@@ -395,9 +399,11 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) sv_attention_narrow_kernel(
                     // Q -> two e4m3 terms; the last segment's products have read the codes
                     constexpr int kPc = D / 8;
                     const int end = rows * kPc;
+                    if (tid == 0)  // read before the barrier above, used again behind the next
+                        ctl.qmax[(nconv & 1u) ^ 1u] = 0;
                     auto piece = [&](int e) {
                         const int row = e / kPc, x = e % kPc;
-                        return *reinterpret_cast<const uint4 *>(smem + (x / 8) * kNarrowPanel + row * 128 + (((x & 7) ^ (row & 7)) * 16));
+                        return *reinterpret_cast<const uint4 *>(smem + (x / 8) * N::kPanel + row * 128 + (((x & 7) ^ (row & 7)) * 16));
                     };
                     unsigned qm = 0;
                     for (int e = tid; e < end; e += kNarrowSoftmax)
@@ -417,20 +423,27 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) sv_attention_narrow_kernel(
                         const int ch = x >> 1, sw = D == 128 ? ch ^ (row & 7) : ch ^ ((row >> 1) & 3);
                         unsigned char *at = qc + row * D + sw * 16 + (x & 1) * 8;
                         *reinterpret_cast<uint2 *>(at) = hi;
-                        *reinterpret_cast<uint2 *>(at + kNarrowRows * D) = l8;
+                        *reinterpret_cast<uint2 *>(at + kN * D) = l8;
                     }
                     fence_async_shared();
                     mbar_arrive(&ctl.q_full);
-                    bar_sync(1, kNarrowSoftmax);  // qmax has been read; it is used again after the next conversion's barriers
-                    if (tid == 0)
-                        ctl.qmax[nconv & 1u] = 0;
                     ++nconv;
                 }
             }
+            return true;
+        };
+        float cq = 0.0f, cq_next;
+        bool more = take(0, cq);
+        while (more) {
+            get_seg(ctl.segs.cur[iseg & 1], seg);
+            ++iseg;
+            const bool draft = seg.draft(), none = seg.none();
+            const int njobs = none ? 0 : seg.n;
             if (nrow <= 0) {
-                bar_sync(1, kNarrowSoftmax);
+                more = take(iseg, cq_next);
                 continue;
             }
+            bool poison = false;
             unsigned long long l2[RW / 2];  // this thread's sums of each row's weights
 #pragma unroll
             for (int k = 0; k < RW / 2; ++k)
@@ -562,7 +575,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) sv_attention_narrow_kernel(
                     }
                     if (q >= 2) {
 #pragma unroll 1
-                        for (int c0 = 0; c0 < 192; c0 += 64)
+                        for (int c0 = 0; c0 < 3 * kN; c0 += kN)
 #pragma unroll 1
                             for (int c1 = 0; c1 < RW; c1 += 8) {
                                 uint32_t o[8];
@@ -596,22 +609,24 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) sv_attention_narrow_kernel(
                             three_terms(w, t[(k - g) / 4], t[2 + (k - g) / 4], t[4 + (k - g) / 4]);
                         }
                     }
-                    const int c = (lo + g) / 8;  // which 8 rows of 64
                     if (dr) {  // key pt's 128 bytes, swizzled
+                        const int c = (lo + g) / 8;  // which 8 rows
                         *reinterpret_cast<uint4 *>(pslot + pt * 128 + ((c ^ (pt & 7)) * 16)) = make_uint4(x[g], x[g + 1], x[g + 4], x[g + 5]);
-                    } else {  // its 64 bytes in each of the three
+                    } else {  // its columns of the three terms, 64 bytes to a swizzled row
 #pragma unroll
-                        for (int part = 0; part < 3; ++part)
-                            *reinterpret_cast<uint2 *>(pslot + part * N::kTerm + pt * 64 + (((c >> 1) ^ ((pt >> 1) & 3)) * 16) + (c & 1) * 8) =
+                        for (int part = 0; part < 3; ++part) {
+                            const int col = part * kN + lo + g;
+                            *reinterpret_cast<uint2 *>(pslot + (col >> 6) * N::kAtom + pt * 64 + ((((col >> 4) & 3) ^ ((pt >> 1) & 3)) * 16) + (col & 8)) =
                                 make_uint2(t[2 * part], t[2 * part + 1]);
+                        }
                     }
                 }
                 if (dr) {  // the new tokens' product writes the first part of O^T only
 #pragma unroll
                     for (int k = 0; k < RW; k += 8) {
                         const uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-                        tmem_st8(tO + 64 + k, zero);
-                        tmem_st8(tO + 128 + k, zero);
+                        tmem_st8(tO + kN + k, zero);
+                        tmem_st8(tO + 2 * kN + k, zero);
                     }
                     tmem_wait_st();
                 }
@@ -623,6 +638,9 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) sv_attention_narrow_kernel(
             }
             if (!none)
                 base += Fills<D, true>::at(seg, seg.n - 1) + (Fills<D, true>::two(draft && seg.n == 1) ? 2 : 1);
+
+            more = take(iseg, cq_next);
+            get_seg(ctl.segs.cur[(iseg + 1) & 1], seg);  // this one again
 
             // ---- epilogue: the slots of these rows ----
             const bool has = slot < njobs;
@@ -694,7 +712,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) sv_attention_narrow_kernel(
                         uint32_t y[24];
 #pragma unroll
                         for (int part = 0; part < 3; ++part)
-                            tmem_ld8_nowait(tmem + lanes + 192 * from + 64 * part + r0, y + 8 * part);
+                            tmem_ld8_nowait(tmem + lanes + 192 * from + kN * part + r0, y + 8 * part);
                         tmem_wait_ld();
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
@@ -718,19 +736,18 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) sv_attention_narrow_kernel(
                             }
                         }
                     } else {
-                        float *dst = piece + (size_t)r0 * D + d;
+                        float *dst = piece + ((size_t)(d >> 2) * prow + r0) * 4 + (d & 3);
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
                             if (r0 + k < rows)
-                                dst[k * D] = o[k];
+                                dst[4 * k] = o[k];
                     }
                 }
             }
             tc_fence_before();
-            if (tid == 0)
-                hand_out_seg(ctl, iseg);
-            bar_sync(1, kNarrowSoftmax);  // the segment is done with
+            bar_sync(6 + group, 256);  // the segment is done with
             tc_fence_after();
+            cq = cq_next;
         }
     }
     finish<kStages, 1>(p, ctl);

@@ -432,6 +432,8 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) sv_attention_narrow_kernel(
             }
             return true;
         };
+        uint32_t vis = 0;    // this warpgroup's rows that see new token pt
+        bool chain = false;  // it is known: without trees it is the same in every segment
         float cq = 0.0f, cq_next;
         bool more = take(0, cq);
         while (more) {
@@ -448,8 +450,9 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) sv_attention_narrow_kernel(
 #pragma unroll
             for (int k = 0; k < RW / 2; ++k)
                 l2[k] = 0;
-            uint32_t vis = 0;  // this warpgroup's rows that see new token pt
-            if (draft && slot == 0) {  // job 0 is slot 0's
+            if (draft && slot == 0 && (p.parent || !chain)) {  // job 0 is slot 0's
+                chain = true;
+                vis = 0;
                 unsigned long long tok = 0;  // tokens that see it
                 const int32_t *par = p.parent ? p.parent + (long long)seg.b * p.T : nullptr;
                 bool bad = false;

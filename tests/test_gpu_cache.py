@@ -278,6 +278,15 @@ def test_attention_many_segments(B, T, G, L, prefix, fmt):
     _check_attention(_attention_case(B + T, B, T, 2, G, 128, L, fmt, prefix=prefix, tree=True, lens=lens))
 
 
+@pytest.mark.parametrize("B,T,H,G,D,L,prefix", [(40, 8, 4, 7, 128, 150, 1100), (41, 5, 5, 3, 64, 129, 2049), (5, 8, 16, 4, 64, 300, 1300),
+                                                (3, 16, 17, 5, 128, 64, 1409), (9, 9, 8, 4, 128, 700, 2000)])
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_attention_long_prefixes(B, T, H, G, D, L, prefix, fmt):
+    """Prefixes of so many tiles that each weighs as two of a sequence's, cut at both of its halves."""
+    lens = [(b * 41 + b * b) % (L + 1) for b in range(B)]
+    _check_attention(_attention_case(B + prefix, B, T, H, G, D, L, fmt, prefix=prefix, tree=T % 2 == 0, lens=lens))
+
+
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
 @pytest.mark.parametrize("B,H,L", [(1, 1, 1), (1, 2, 1152), (1, 2, 1281), (19, 8, 1152), (51, 3, 130), (152, 1, 1281)])
 def test_attention_few_segments_whole_and_cut(B, H, L, fmt):

@@ -155,7 +155,8 @@ typedef struct {
  * too small; SV_ERR_SHAPE: head_dim other than 64 and 128; SV_ERR_DTYPE:
  * unknown format; SV_ERR_TOO_LARGE: B * T * heads_q or a count of tiles past
  * 2^31 - 1; SV_ERR_CUDA: a driver or runtime call failed.  B == 0 enqueues nothing.
- * Two kernel launches.
+ * One kernel launch for a few short sequences without a prefix, two otherwise, four with an e4m3 prefix
+ * that more than 256 rows (B * T * heads_q / heads_kv) share.
  */
 enum { SV_ATTN_BAD_LEN = 1, SV_ATTN_BAD_TREE = 2, SV_ATTN_TIMEOUT = 4 };
 

@@ -5,8 +5,8 @@
 // With 8-bit keys and values a tile's HBM time halves, and the products of
 // attention.cu (rows on the tensor cores' M side, padded to 128) take longer than
 // that.  Here they are turned around: S^T = K Q^T puts a tile's 128 keys on M and the
-// rows on N = 64, and O^T = V^T P^T the head's channels on M.  That halves
-// the matrix work, the softmax uses all lanes whatever the number of rows
+// rows, padded to 16, 32 or 48, on N, and O^T = V^T P^T the head's channels on M.  That
+// saves more than half of the matrix work, the softmax uses all lanes whatever the number of rows
 // (thread = key), a key's scales are registers instead of table reads, and the
 // mask of the length is a property of the thread.  What it costs: a row's maximum
 // lies across threads.  It is not looked for: a reference only has to keep the weights
@@ -16,11 +16,9 @@
 // threads once, at the segment's end.
 //
 // P^T goes to shared memory (the B operand cannot come from tensor memory) as three
-// e5m2 terms side by side along N, so that one instruction of N = 192 reads V once
+// e5m2 terms side by side along N, so that one instruction reads V once
 // for all three; O^T is then the sum of three column ranges.  The two e4m3 terms
-// of Q add up in place.  Shared-memory traffic of a tile (128 keys of D = 128; the limit
-// is 128 B a cycle): 32 KB by TMA, 48 + 40 read by the products, 24 of P: 1150 cycles
-// against 1400 of HBM time.
+// of Q add up in place.
 //
 // Four warpgroups do the softmax: two slots, which take alternate tiles (what bounds a warpgroup is
 // its chain of dependent instructions for a tile), each with its own S^T, P^T and O^T, and in each two
@@ -29,8 +27,16 @@
 // memory latency.
 //   warps 0-15   warpgroup w: rows RW (w >> 1) .., slot w & 1; thread = key, then channel
 //   warps 16-19  producer, MMA issuer, clearing warp, as in attention.cu; the keys' scales into shared memory
-// TMEM: O^T of the slots at columns 0 and 192 (three parts of 64), S^T at 384 and 448.
+// TMEM: O^T of the slots at columns 0 and 192 (three parts of kN), S^T at 384 and 448.
 // Walk, ring, stretches, clearing and joining are attention.cu's.
+//
+// Measured, us a tile of each SM (HBM alone: 0.74): 0.79 with 14 rows, 0.87 with 28, 1.10 with
+// 42 (16384 keys a sequence); a segment costs 3 to 8 us besides (its last product, its epilogue and its first
+// tiles are not covered by others).  256 chains of 6 over up to 4096 keys (566 MB) take 223 us, 2
+// sequences of 131072 keys with single tokens 31 (20 of HBM).  With 42 rows a slot's tile is 3200
+// cycles of softmax, at 38 % of the issue slots; N of 64 whatever the rows: 118 us instead of 111
+// (14 rows); a slot's next scores issued ahead of its product: 165 instead of 150 (42 rows); the codes of Q
+// made after the epilogue instead of before it: 11 us a segment.
 #pragma once
 
 namespace {

@@ -146,7 +146,9 @@ typedef struct {
  * whose parent entries break their rule SV_ATTN_BAD_TREE; its out and lse are
  * NaN, and nothing out of range is read.  Keys and values that a token
  * does not see do not matter, NaN and infinities among them; a NaN or infinity
- * in v_new makes the tokens that see it NaN in all columns.  SV_ATTN_TIMEOUT:
+ * in v_new makes the tokens that see it NaN in all columns.  A NaN in a row of q makes
+ * that row NaN, an infinity there leaves its result open; no other row changes.
+ * out overlaps none of the inputs.  SV_ATTN_TIMEOUT:
  * a bounded wait inside the kernel gave up; the outputs are then invalid.
  *
  * SV_ERR_INVALID_ARG: a NULL args, sizes below 1 (max_len and prefix_len below

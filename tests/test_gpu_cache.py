@@ -287,6 +287,46 @@ def test_attention_long_prefixes(B, T, H, G, D, L, prefix, fmt):
     _check_attention(_attention_case(B + prefix, B, T, H, G, D, L, fmt, prefix=prefix, tree=T % 2 == 0, lens=lens))
 
 
+@pytest.mark.parametrize("B,T,H,G,D,L,prefix", [(3, 40, 2, 8, 64, 100, 300), (1, 128, 1, 300, 64, 130, 0), (2, 128, 1, 96, 128, 3, 129),
+                                                (600, 1, 1, 1, 128, 5, 1)])
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_attention_many_rows(B, T, H, G, D, L, prefix, fmt):
+    """Sequences of several blocks of rows, and many of one row behind one prefix key."""
+    lens = [(b * 41 + L) % (L + 1) for b in range(B)]
+    _check_attention(_attention_case(B + G, B, T, H, G, D, L, fmt, prefix=prefix, tree=True, lens=lens))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_attention_of_more_sequences_than_16_bits_count(fmt):
+    B, keep = 66000, [0, 1, 2, 1023, 32767, 32768, 65535, 65536, 65998, 65999]
+    c = _attention_case(33, B, 1, 1, 2, 64, 3, fmt, lens=[b % 4 for b in range(B)])
+    out, lse, st = _attention_gpu(c)
+    assert st == 0
+    few = {k: (None if v is None else v.view(torch.uint8)[keep].view(FP8) if v.dtype == FP8 else v[keep])
+           for k, v in c.items()}
+    o, ll, tol, tol_lse = ref.attention(few["q"], few["k"], few["v"], few["lens"], few["k_new"], few["v_new"],
+                                        few["parent"], None, None, few["ks"], few["vs"])
+    ref.assert_close(out[keep], o, tol, "out")
+    ref.assert_close(lse[keep], ll, tol_lse, "lse")
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("T,G", [(2, 4), (5, 5), (3, 13), (16, 5)])
+def test_attention_a_row_that_is_not_finite_leaves_the_others(T, G, fmt):
+    """NaN and infinities in one query row: every other row's result is what it is without them, bit for bit."""
+    c = _attention_case(35, 3, T, 2, G, 128, 500, fmt, tree=True, lens=[500, 130, 7])
+    want = _attention_gpu(c)
+    for bad in (math.nan, math.inf):
+        d = dict(c, q=c["q"].clone())
+        d["q"][1, T - 1, G, 5] = bad
+        got = _attention_gpu(d)
+        rest = torch.ones(want[1].shape, dtype=torch.bool)
+        rest[1, T - 1, G] = False
+        assert torch.equal(got[0][rest], want[0][rest]) and torch.equal(got[1][rest], want[1][rest])
+        if math.isnan(bad):
+            assert torch.isnan(got[0][1, T - 1, G].float()).all()
+
+
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
 @pytest.mark.parametrize("B,H,L", [(1, 1, 1), (1, 2, 1152), (1, 2, 1281), (19, 8, 1152), (51, 3, 130), (152, 1, 1281)])
 def test_attention_few_segments_whole_and_cut(B, H, L, fmt):

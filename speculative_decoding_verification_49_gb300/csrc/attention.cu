@@ -1372,8 +1372,10 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
                 const size_t orow = (size_t)tok * p.Hq + seg.h * p.G + (Rg - tok * p.G);
                 f_own *= scl;
                 f_oth *= scl;
+                const unsigned long long own2 = pack2(f_own, f_own), oth2 = pack2(f_oth, f_oth);
 #pragma unroll 1
                 for (int c0 = cs; c0 < ce; c0 += 32) {
+                    // a slot that had jobs holds finite sums but for what seen values put there: nothing is left out here
                     uint32_t x[32];
                     float o[32];
 #pragma unroll
@@ -1383,15 +1385,15 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
                         tmem_ld32_nowait(tO + c0, x);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            o[k] += f_own == 0.0f ? 0.0f : f_own * __uint_as_float(x[k]);
+                        for (int k = 0; k < 32; k += 2)
+                            unpack2(mul2(pack2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), own2), o[k], o[k + 1]);
                     }
                     if (!pair && other) {
                         tmem_ld32_nowait((s ? tO - 128 : tO + 128) + c0, x);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            o[k] += f_oth == 0.0f ? 0.0f : f_oth * __uint_as_float(x[k]);
+                        for (int k = 0; k < 32; k += 2)
+                            unpack2(fma2(pack2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), oth2, pack2(o[k], o[k + 1])), o[k], o[k + 1]);
                     }
                     if (valid_row) {
                         if (direct) {

@@ -727,7 +727,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) sv_attention_narrow_kernel(
                         for (int k = 0; k < 8; ++k) {
                             const float a = ctl.fac[from][r0 + k];
                             const float v = (__uint_as_float(y[k]) + __uint_as_float(y[8 + k])) + __uint_as_float(y[16 + k]);
-                            o[k] += a == 0.0f ? 0.0f : a * v;
+                            o[k] += a * v;
                         }
                     }
                     if (direct) {

@@ -1099,16 +1099,29 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
             bool convert = false;             // Q has yet to go from bf16 to codes
             if (!none) {
                 if (!seg.tq) {
+                    // a thread's rows are `down` apart: their (sequence, token, head) is stepped, not divided for
+                    const int x = q_from % kPc, down = q_step / kPc;
+                    const int dtok = down / p.G, dg = down - dtok * p.G, db = dtok / p.T, dt = dtok - db * p.T;
+                    int row = q_from / kPc, tok = (row0 + row) / p.G, g = row0 + row - tok * p.G, b = tok / p.T, t = tok - b * p.T;
+                    const __nv_bfloat16 *from = p.q + seg.h * p.G * D + x * 8;
 #pragma unroll 4
                     for (int e = q_from; e < q_end; e += q_step) {
-                        const int row = e / kPc, x = e % kPc;
                         uint4 v = make_uint4(0, 0, 0, 0);
-                        if (row < rows) {
-                            const int R = row0 + row, tok = R / p.G, b = tok / p.T;
-                            v = __ldg(reinterpret_cast<const uint4 *>(p.q + b * p.q_sb + (long long)(tok - b * p.T) * p.q_st +
-                                                                      (seg.h * p.G + (R - tok * p.G)) * D + x * 8));
-                        }
+                        if (row < rows)
+                            v = __ldg(reinterpret_cast<const uint4 *>(from + b * p.q_sb + t * p.q_st + g * D));
                         *q_piece(row, x) = v;
+                        row += down;
+                        g += dg;
+                        t += dt;
+                        b += db;
+                        if (g >= p.G) {
+                            g -= p.G;
+                            ++t;
+                        }
+                        if (t >= p.T) {
+                            t -= p.T;
+                            ++b;
+                        }
                     }
                 }
                 if (seg.tq && E4) {

@@ -1042,9 +1042,48 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
         uint32_t ntq = 0;            // segments whose Q came by TMA
         bool by_threads = false;     // earlier ones came otherwise
         uint32_t iseg = 0;
+        constexpr int kPc = D / 8;  // 16-byte pieces of a row of Q
+        // Starts the copies of Q's rows, dealt to the slot's threads, or to both slots' when they share the tile; zeros behind them.
+        auto load_q = [&](const Seg &n) {
+            const bool two = n.pair();
+            const int rows = n.slot_rows(s), row0 = n.row0 + (two ? kTile * s : 0);
+            const int first = two ? pt : tid, threads = two ? 128 : 256, end = cdiv(rows * kPc, 32) * 32;  // whole warps
+            unsigned char *qt = smem + (two ? s : 0) * C::kQTile;
+            // a thread's rows are `down` apart: their (sequence, token, head) is stepped, not divided for
+            const int x = first % kPc, down = threads / kPc;
+            const int dtok = down / p.G, dg = down - dtok * p.G, db = dtok / p.T, dt = dtok - db * p.T;
+            int row = first / kPc, tok = (row0 + row) / p.G, g = row0 + row - tok * p.G, b = tok / p.T, t = tok - b * p.T;
+            const __nv_bfloat16 *from = p.q + n.h * p.G * D + x * 8;
+#pragma unroll 4
+            for (int e = first; e < end; e += threads) {
+                async_copy16(qt + (x / 8) * kPanel + row * 128 + (((x & 7) ^ (row & 7)) * 16),
+                             row < rows ? from + b * p.q_sb + t * p.q_st + g * D : p.q, row < rows);
+                row += down;
+                g += dg;
+                t += dt;
+                b += db;
+                if (g >= p.G) {
+                    g -= p.G;
+                    ++t;
+                }
+                if (t >= p.T) {
+                    t -= p.T;
+                    ++b;
+                }
+            }
+        };
+        auto q_loaded = [&]() {
+            async_copies_wait();
+            fence_async_shared();
+            mbar_arrive(&ctl.q_full);
+        };
         if (tid == 0)
             hand_out_seg(ctl, 0);
         bar_sync(1, kSoftmaxThreads);
+        if (!E4 && get_seg(ctl.segs.cur[0], seg) && !seg.none() && !seg.tq) {
+            load_q(seg);
+            q_loaded();
+        }
         while (get_seg(ctl.segs.cur[iseg & 1], seg)) {
             ++iseg;
             const bool pair = seg.pair(), draft = seg.draft(), none = seg.none();
@@ -1057,8 +1096,7 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
             float cq = p.c;  // factor of an e4m3 job's scores
             const uint32_t qb = seg.tq ? ntq & 1u : 0u;
             unsigned char *qt = smem + (pair ? s : qb) * C::kQTile;
-            // the 16-byte pieces of Q's rows, dealt to the slot's threads, or to both slots' when they share the tile
-            constexpr int kPc = D / 8;  // pieces of a row
+            // the pieces as load_q deals them
             const int q_from = pair ? pt : tid, q_step = pair ? 128 : 256;
             const int q_end = cdiv(rows * kPc, 32) * 32;  // whole warps
             auto q_piece = [&](int row, int x) {
@@ -1098,31 +1136,9 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
             uint32_t seen[4] = {0, 0, 0, 0};  // new tokens that this row sees; only ever indexed by constants
             bool convert = false;             // Q has yet to go from bf16 to codes
             if (!none) {
-                if (!seg.tq) {
-                    // a thread's rows are `down` apart: their (sequence, token, head) is stepped, not divided for
-                    const int x = q_from % kPc, down = q_step / kPc;
-                    const int dtok = down / p.G, dg = down - dtok * p.G, db = dtok / p.T, dt = dtok - db * p.T;
-                    int row = q_from / kPc, tok = (row0 + row) / p.G, g = row0 + row - tok * p.G, b = tok / p.T, t = tok - b * p.T;
-                    const __nv_bfloat16 *from = p.q + seg.h * p.G * D + x * 8;
-#pragma unroll 4
-                    for (int e = q_from; e < q_end; e += q_step) {
-                        uint4 v = make_uint4(0, 0, 0, 0);
-                        if (row < rows)
-                            v = __ldg(reinterpret_cast<const uint4 *>(from + b * p.q_sb + t * p.q_st + g * D));
-                        *q_piece(row, x) = v;
-                        row += down;
-                        g += dg;
-                        t += dt;
-                        b += db;
-                        if (g >= p.G) {
-                            g -= p.G;
-                            ++t;
-                        }
-                        if (t >= p.T) {
-                            t -= p.T;
-                            ++b;
-                        }
-                    }
+                if (E4 && !seg.tq) {
+                    load_q(seg);
+                    async_copies_wait();
                 }
                 if (seg.tq && E4) {
                     if (ntq == 0 && by_threads && lane == 0) {  // the earlier segments' part of the first phase
@@ -1136,14 +1152,16 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
                 }
                 ntq += seg.tq;
                 by_threads |= !seg.tq;
-                if (!E4 || draft) {
-                    if (!seg.tq) {
-                        fence_async_shared();
-                        mbar_arrive(&ctl.q_full);
+                if constexpr (E4) {
+                    if (draft) {
+                        if (!seg.tq) {
+                            fence_async_shared();
+                            mbar_arrive(&ctl.q_full);
+                        }
+                        convert = seg.n > 1;
+                    } else {
+                        to_codes();
                     }
-                    convert = E4 && seg.n > 1;
-                } else {
-                    to_codes();
                 }
                 if (draft) {
                     const int t = min((seg.rb * 2 * kTile + (pair ? kTile * s : 0) + r) / p.G, p.T - 1);
@@ -1340,8 +1358,21 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
 
             // ---- epilogue: join the slots, write ----
             const bool has = s < njobs, other = (1 - s) < njobs;
+            bool next_q = false;
+            if constexpr (!E4) {
+                // the next segment's Q ahead of this one's epilogue, so that its first scores are there when that is done
+                if (tid == 0)
+                    hand_out_seg(ctl, iseg);
+                bar_sync(1, kSoftmaxThreads);  // and this one's Q has been read: all its scores are complete
+                Seg n;
+                next_q = get_seg(ctl.segs.cur[iseg & 1], n) && !n.none() && !n.tq;
+                if (next_q)
+                    load_q(n);
+            }
             if (has)
                 await(ctl, &ctl.o_full[s], nj - 1);
+            if (next_q)
+                q_loaded();
             if (draft) {
                 await(ctl, &ctl.poison_full, npois++);
 #pragma unroll
@@ -1429,7 +1460,7 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
             tc_fence_before();
             if (E4 && pt == 0)
                 ctl.qmax[s] = 0;  // read last before this segment's products
-            if (tid == 0)
+            if (E4 && tid == 0)
                 hand_out_seg(ctl, iseg);
             bar_sync(1, kSoftmaxThreads);  // O has been read by both slots, the exchange may be overwritten
             tc_fence_after();

@@ -87,6 +87,18 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t *bar, uint32_t parity
     }
 }
 
+// ---- 16-byte copies global -> shared memory by single threads; zeros where `there` is false ----
+__device__ __forceinline__ void async_copy16(void *dst, const void *src, bool there)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+
+// Waits for this thread's.
+__device__ __forceinline__ void async_copies_wait()
+{
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
 // ---- TMA: 1-D bulk copy global -> this CTA's shared memory ------------------
 // dst, src 16-byte aligned, bytes a multiple of 16; completion is signalled on
 // `bar` as transaction bytes.

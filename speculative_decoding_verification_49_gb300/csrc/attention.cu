@@ -60,15 +60,15 @@
 //
 // What bounds it (152 SMs, 6780 GB/s and 1933 TFLOP/s of plain copies and matrix products):
 //   256 chains of 8 over up to 2048 bf16 keys, 28 / 4 heads: 109 us, HBM at 0.77
-//   (569 MB); 64 trees of 16 over up to 8192: 106, 0.79.  A segment's 17 us are
-//   13 of tiles and 3 of epilogue, under which the ring refills.
-//   64 x 8 tokens over a prefix of 8192: 86 us.  A tile of 256 rows takes 4000 cycles
-//   where its products take 2048: one warp issues them between the softmax of two
-//   slots, whose warps run at 28 % of the issue slots, waiting for each other and
-//   for tensor memory; a third slot has no room in it.
+//   (569 MB); 64 trees of 16 over up to 8192: 107, 0.77.  A segment's 14 us are
+//   11 of tiles and 3 of epilogue, under which the ring refills.
+//   64 x 8 tokens over a prefix of 8192: 76 us.  A tile of 256 rows takes 3700 cycles
+//   where its products take 2048: the issuing warp is held by them for 1930, waits
+//   560 for weights and 520 for tiles, and its own steps take 650; the softmax warps
+//   run at 28 % of the issue slots; a third slot has no room in tensor memory.
 //   The rolled softmax loops are measured: one unrolled pass with the scores, or the
 //   weights, kept in registers takes 126 us for the chains and 109 for the prefix
-//   (straight-line code of that length is fetched slower than it runs); loads of
+//   (113 and 102 then; straight-line code of that length is fetched slower than it runs); loads of
 //   tensor memory a chunk ahead change nothing.
 //
 // Every wait is bounded (2 s); a kernel that gives up says so in *status.
@@ -1275,8 +1275,9 @@ __global__ void __launch_bounds__(kThreads, 1) sv_attention_kernel(const __grid_
                         mx *= p.c;
                     const bool grow = mx > mu + C::kSlack || (mu == -INFINITY && mx > mu);
                     if (__any_sync(0xffffffffu, grow)) {
-                        const float mn = fmaxf(mu, mx);
-                        const float f = mu == -INFINITY ? 0.0f : ex2(mu - mn);
+                        // a row moves for itself alone: its result depends on no other row, nor on what lies behind the last one
+                        const float mn = grow ? fmaxf(mu, mx) : mu;
+                        const float f = !grow ? 1.0f : mu == -INFINITY ? 0.0f : ex2(mu - mn);
                         mu = mn;
                         l *= f;
                         if (q >= 2) {  // O holds earlier tiles: their product must be complete
@@ -1812,12 +1813,13 @@ bool plan(const sv_attention_args &a, Plan &w)
     // stretches alike.  Measured: 256 chains of 8 over up to 2048 keys 124, 116, 114 us with 1, 2, 3; of 6 over 4096 e4m3
     // keys 243, 232, 227, 227 us with 3, 4, 5, 6.
     w.split = a.format == SV_KV_E4M3 && a.prefix_len > 0 && w.nbp >= 2;
-    w.seg_cost = a.format == SV_KV_E4M3 && !(a.prefix_len > 0 && !w.split) && seq_rows <= kNarrowMost ? 6 : 3;
+    w.seg_cost = a.format == SV_KV_E4M3 && !(a.prefix_len > 0 && !w.split) && seq_rows <= kNarrowMost ? 6 : a.prefix_len > 0 ? 4 : 3;
     // A prefix tile is 256 rows' work, twice that of a sequence's tile of up to 128 rows beside it.  64 sequences' 56 rows
-    // over a prefix of 8192 keys: with one unit for either and costs of 1 the CTAs' times lie between 0.7 and 1.2 of the
-    // mean and the call takes 101.9 us; with two units and costs of 3 and 6, 95.6.  On a line of its own (128 sequences' 112
-    // rows over 2048 keys) a segment costs 8 tiles' time: 180.5 us with 1, 178.4 with 3, 172.2 with 8.
-    w.prefix_cost = w.split ? 8 : 6;
+    // over a prefix of 8192 keys: with one unit for either and costs of 1 the CTAs' times lay between 0.7 and 1.2 of the
+    // mean (101.9 us; 95.6 with two units and costs of 3 and 6).  Costs of a sequence's and a prefix's segment since: 2 and 5
+    // 86.1, 3 and 6 78.3, 3 and 3 77.3, 4 and 4 76.0, 4 and 8 75.6.  On a line of its own (128 sequences' 112 rows over
+    // 2048 keys) a prefix's: 138.2 us with 3 or 4, 136.9 with 5, 140.0 with 8, 141.6 with 10.
+    w.prefix_cost = w.split ? 5 : 6;
     w.prefix_two = !w.split && rows > kTile && seq_rows <= kTile && 2 * a.heads_kv * w.nbp * w.ntp >= 2 * kMaxCtas;
     w.UP = a.prefix_len > 0 ? a.heads_kv * w.nbp * (((int64_t)w.ntp << w.prefix_two) + w.prefix_cost) : 0;  // below 2^31 * 2^25
     if (a.prefix_len > big / (a.heads_kv * a.head_dim))

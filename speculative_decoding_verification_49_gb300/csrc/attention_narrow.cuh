@@ -32,7 +32,7 @@
 //
 // Measured, us a tile of each SM (HBM alone: 0.74): 0.79 with 14 rows, 0.87 with 28, 1.10 with
 // 42 (16384 keys a sequence); a segment costs 3 to 8 us besides (its last product, its epilogue and its first
-// tiles are not covered by others).  256 chains of 6 over up to 4096 keys (566 MB) take 223 us, 2
+// tiles are not covered by others).  256 chains of 6 over up to 4096 keys (566 MB) take 219 us, 2
 // sequences of 131072 keys with single tokens 31 (20 of HBM).  With 42 rows a slot's tile is 3200
 // cycles of softmax, at 38 % of the issue slots; N of 64 whatever the rows: 118 us instead of 111
 // (14 rows); a slot's next scores issued ahead of its product: 165 instead of 150 (42 rows); the codes of Q

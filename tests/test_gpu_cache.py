@@ -493,6 +493,24 @@ def test_attention_repeats_bit_for_bit_and_in_graphs_on_two_streams(fmt):
         assert torch.equal(o.cpu(), w[0])
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("T,G,prefix", [(8, 7, 0), (8, 7, 300), (5, 3, 0), (9, 5, 0), (13, 5, 0)])
+def test_attention_does_not_depend_on_what_ran_before(T, G, prefix, fmt):
+    """Rows behind a sequence's last one hold what an earlier kernel left in shared memory: the result is the same bit for bit."""
+    c = _attention_case(41, 40, T, 2, G, 128, 900, fmt, prefix=prefix, tree=True)
+    c["q"] *= 4                      # scores that move the references now and then
+    other = [_attention_case(42, 40, 16, 2, 8, 128, 300, "bf16", tree=True) for _ in range(2)]
+    other[0]["q"] *= 1000
+    other[1]["q"] *= 0
+    _attention_gpu(other[1])
+    want = _attention_gpu(c)
+    for _ in range(3):
+        for o in other:
+            _attention_gpu(o)
+            got = _attention_gpu(c)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_attention_over_a_cache_past_32_bit_offsets():
     """5 GB a plane: the last sequences' rows lie past 2^32 bytes (and 2^31 elements)."""
     B, L, H, D, G, T = 41, 131072, 4, 128, 2, 2
